@@ -20,7 +20,8 @@ SOURCES = ["moe_api.hip", "moe_align.hip", "moe_prepare.hip", "moe_gemm.hip", "m
            "moe_gemm_nvfp4.hip", "moe_gemm_mxfp4.hip", "moe_gemm_int4zp.hip", "moe_gemm_stream_int4.hip",
            "moe_gemm_stream_nvfp4.hip", "moe_gemm_stream_mxfp4.hip", "moe_gemm_stream_int4zp.hip",
            "moe_gemm_int4zpf.hip", "moe_gemm_stream_int4zpf.hip",
-           "moe_act_combine.hip", "moe_requant.hip"]
+           "moe_act_combine.hip", "moe_requant.hip",
+           "moe_fp8_quant.hip", "moe_w8a8.hip", "moe_bf16.hip", "moe_bf16_grad.hip"]
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
