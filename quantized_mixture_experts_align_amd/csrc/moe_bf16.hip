@@ -19,6 +19,6 @@ extern "C" int moe_bf16_gemm(const uint16_t* A, int64_t a_rows, int64_t lda, con
   if (rc) return rc;
   const BlockGemmArgs a{reinterpret_cast<const uint8_t*>(A), lda * 2, reinterpret_cast<const uint8_t*>(W), nullptr, 0,
                         nullptr, bias, C, ldc, sorted_token_ids, expert_ids, num_tokens_post_padded, (int32_t)numel,
-                        top_k, block_m, N, K * 2, E, 0};
+                        top_k, block_m, N, K * 2, E, 0, 0, 0, 0};
   return launch_block_gemm<Bf16Type>(fn, a, cap_blocks, stream);
 }

@@ -243,8 +243,8 @@ static int check_grad(const char* fn, const void* dC, int64_t ld_dc, int32_t E, 
                       int32_t top_k, int32_t block_m) {
   MOE_REQUIRE(E >= 1 && N >= 1 && K >= 1, MOE_EINVAL, "%s: E=%d N=%d K=%d", fn, E, N, K);
   MOE_REQUIRE(E <= 512, MOE_EUNSUPPORTED, "%s: %d experts (at most 512)", fn, E);
-  MOE_REQUIRE(N % 8 == 0 && K % 8 == 0 && N <= (1 << 24) && K <= (1 << 24), MOE_EUNSUPPORTED,
-              "%s: N=%d and K=%d must be multiples of 8 (at most 2^24)", fn, N, K);
+  MOE_REQUIRE(N % 8 == 0 && K % 8 == 0 && N <= (1 << 20) && K <= (1 << 20), MOE_EUNSUPPORTED,
+              "%s: N=%d and K=%d must be multiples of 8 (at most 2^20)", fn, N, K);
   MOE_REQUIRE(numel >= 0 && top_k >= 1 && block_m >= 1 && block_m <= 256, MOE_EINVAL,
               "%s: numel=%lld top_k=%d block_m=%d (1..256)", fn, (long long)numel, top_k, block_m);
   MOE_REQUIRE(numel < (1 << 30), MOE_EUNSUPPORTED, "%s: numel=%lld", fn, (long long)numel);

@@ -35,7 +35,8 @@ struct BlockGemmArgs {
   const int32_t* eids;
   const int32_t* ntpp;
   int32_t numel, top_k, block_m, N, Kb, E;
-  int32_t group_m;        // tile kernel: align blocks per XCD workgroup group
+  int32_t tiles, group_m, group_n;  // tile kernel: tiles of rows; tiles and strips of an XCD's unit
+  int32_t cap_blocks;     // most blocks the align can have made
 };
 
 struct Fp8Type {
@@ -83,10 +84,8 @@ __device__ __forceinline__ f32x4_t mfma_step(Fp8Type, const Frag& w, const Frag&
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// The slot at position p of block b, or -1 for padding.
-__device__ __forceinline__ int slot_of(const BlockGemmArgs& a, int b, int p) {
-  if (p >= a.block_m) return -1;
-  const int64_t at = (int64_t)b * a.block_m + p;
+// The slot of sorted entry `at` (dense: row `at`), or -1 for padding.
+__device__ __forceinline__ int slot_at(const BlockGemmArgs& a, int64_t at) {
   const int64_t s = a.sorted ? a.sorted[at] : at;
   return s >= 0 && s < a.numel ? (int)s : -1;
 }
@@ -109,7 +108,7 @@ __global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArg
     e = a.eids[b];
     if (e < 0 || e >= a.E) return;
   }
-  const int slot = slot_of(a, b, lane & 15);
+  const int slot = (lane & 15) < a.block_m ? slot_at(a, (int64_t)b * a.block_m + (lane & 15)) : -1;
   if (__ballot(slot >= 0) == 0) return;  // (the same in every wave)
 
   const int KT = (a.Kb + kStepBytes - 1) / kStepBytes;
@@ -194,8 +193,8 @@ __global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArg
 // step's barrier), so that a store instruction covers whole segments of 32 * NG bytes of a row with
 // 16 bytes a lane.  row_ptr(r) is where row r starts, or null.
 template <int NG, int MG, typename OUT, typename RowPtr>
-__device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg, uint8_t* smem, int smem_bytes, int w,
-                                            int lane, int n0, int N, bool wide, RowPtr row_ptr) {
+__device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg, uint8_t* smem, int w, int lane,
+                                            int n0, int N, bool wide, RowPtr row_ptr) {
   if constexpr (sizeof(OUT) == 4) {
 #pragma unroll
     for (int h = 0; h < MG; ++h) {
@@ -240,6 +239,7 @@ __device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg
 #pragma unroll
       for (int r0 = 0; r0 < 16; r0 += RPI) {
         const int r = r0 + lane / CHUNKS;
+        if (RPI > 16 && r >= 16) continue;  // (one tile: 32 rows' worth of lanes, 16 rows)
         OUT* row = row_ptr(h * 16 + r);
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(wl + r * PITCH + 16 * j);
         if (row && n0 + 8 * j < N) *reinterpret_cast<u32x4_t*>(row + n0 + 8 * j) = v;
@@ -254,9 +254,12 @@ __device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg
 // Live 16-row groups of a block whose slots are in s_slot[BM] (live rows come first).
 template <int BM>
 __device__ __forceinline__ int live_groups(const int* s_slot, int lane) {
-  const uint64_t m0 = __ballot(lane < BM && s_slot[lane < BM ? lane : 0] >= 0);
-  const uint64_t m1 = BM > 64 ? __ballot(s_slot[BM > 64 ? 64 + lane : 0] >= 0) : 0ull;
-  const int last = m1 ? 127 - __clzll((long long)m1) : (m0 ? 63 - __clzll((long long)m0) : -1);
+  int last = -1;
+#pragma unroll
+  for (int r = 0; r < BM; r += 64) {
+    const uint64_t m = __ballot(r + lane < BM && s_slot[r + lane < BM ? r + lane : 0] >= 0);
+    if (m) last = r + 63 - __clzll((long long)m);
+  }
   return __builtin_amdgcn_readfirstlane((last + 16) >> 4);
 }
 
@@ -271,98 +274,177 @@ __device__ __forceinline__ void dma_from(const uint8_t* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
 }
 
-// Workgroup = 4 waves over up to 16 * MG rows of one block x 64 * NG weight rows; wave w owns NG
-// 16-row tiles and all the rows.  The waves share the activations, so these go through LDS (two
-// stages, written by direct loads in operand order: a ds_read_b128 per lane and half operand); a
-// weight tile is used by one wave only and goes straight to its registers, one step ahead.  With all
-// of them in LDS a step of 128 rows would move 144 KB through it, more than its 128 bytes a clock
-// allow beside the MFMAs; without the weights it is 80 KB.
-template <typename T, int MG, int NG>
-__global__ __launch_bounds__(256, 2) void block_gemm_tile_kernel(BlockGemmArgs a) {
-  constexpr int BM = 16 * MG;
-  constexpr int XL = MG / 2;                       // activation loads per thread and step
-  constexpr int XB = 2 * MG * 1024;                // bytes of activations per step
-  constexpr int STAGE = XB + (T::kScaled ? BM * 4 : 0);
-  constexpr int EPI = 4 * 16 * (32 * NG + 16);
-  constexpr int SMEM = 2 * STAGE > EPI ? 2 * STAGE : EPI;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
+// Launch index -> (tile of rows, strip of weight rows).  A unit of group_m tiles x group_n strips runs
+// on one XCD, so that its workgroups share activations and weights in that XCD's L2; the units go
+// round the XCDs, strips first, so that the eight that run side by side share tiles of rows.
+__host__ __device__ inline void unit_tile(int P, int strips, int group_m, int group_n, int& mb, int& strip) {
+  const int U = group_m * group_n, across = (strips + group_n - 1) / group_n;
+  const int j = P / kXcds, u = j / U * kXcds + P % kXcds, r = j % U;
+  mb = u / across * group_m + r % group_m;
+  strip = u % across * group_n + r / group_m;
+}
+
+// The workgroup's tile when tiles of BM entries are made of several blocks: an expert's blocks follow
+// each other, and the ones whose number within the expert is a multiple of BM / block_m start a tile.
+// Tile t's first block and its entries (0 behind the last tile).  Every thread calls it; `lds` holds an
+// int for each block of the capacity.  (The tiles are counted here, by each workgroup for itself, so
+// that no launch has to come before and the live tiles lie side by side for the XCDs.)
+__device__ __forceinline__ int merged_tile(const BlockGemmArgs& a, int cap_blocks, int BM, int t, int* lds, int* block) {
+  const int lane = threadIdx.x & 63, per = BM / a.block_m;
+  for (int i = threadIdx.x; i < cap_blocks; i += blockDim.x) lds[i] = a.eids[i];
+  __syncthreads();
+  const int c = (cap_blocks + 63) / 64, i0 = min(lane * c, cap_blocks), i1 = min(i0 + c, cap_blocks);
+  auto at = [&](int i) { return i >= 0 && i < cap_blocks ? lds[i] : -1; };
+  auto live = [&](int e) { return e >= 0 && e < a.E; };
+  int begin = -1;  // the last block of the lane's share that begins an expert
+  for (int i = i0; i < i1; ++i)
+    if (at(i) != at(i - 1)) begin = i;
+  int before = __shfl_up(begin, 1);
+  if (lane == 0) before = 0;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(before, d);
+    if (lane >= d) before = max(before, o);
+  }
+  int tiles = 0, from = max(before, 0);
+  for (int i = i0; i < i1; ++i) {
+    if (at(i) != at(i - 1)) from = i;
+    tiles += live(at(i)) && (i - from) % per == 0;
+  }
+  int sum = tiles;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  int found = -1, left = t - (sum - tiles);
+  if (left >= 0 && left < tiles) {
+    from = max(before, 0);
+    for (int i = i0; i < i1 && found < 0; ++i) {
+      if (at(i) != at(i - 1)) from = i;
+      if (live(at(i)) && (i - from) % per == 0 && left-- == 0) found = i;
+    }
+  }
+  const uint64_t who = __ballot(found >= 0);
+  if (!who) return 0;
+  found = __shfl(found, __builtin_ctzll(who));
+  const int e = at(found);
+  int n = 1;
+  while (n < per && at(found + n) == e) ++n;
+  *block = __builtin_amdgcn_readfirstlane(found);
+  return __builtin_amdgcn_readfirstlane(n) * a.block_m;
+}
+
+// Workgroup = WM x WN waves over BM = 16 * MG * WM rows of one block x BN = 16 * NG * WN weight rows;
+// wave (wm, wn) owns MG 16-row groups and NG 16-row weight tiles.
+//
+// Both operands go through LDS, kStages steps deep, written by direct global -> LDS loads.  A staged
+// row is its 128 bytes of the step in eight 16-byte pieces, piece p at place p ^ (row & 7): the eight
+// lanes that load a row then ask for one whole cache line (an operand loaded straight to registers
+// has its adjacent lanes in different rows, a cache line each: 64 address cycles a load instead of
+// 16, which held the first form of this kernel to a third of the speed), and the eight lanes that a
+// ds_read_b128 serves at once, eight rows of the same piece, hit different banks.
+//
+// Step kt + kStages - 1 is requested when step kt starts.  The step's closing wait and barrier come
+// before the products of its last row group, whose operands are in registers by then: the first
+// operands of the next step are read from LDS behind those products.
+template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge>
+// (two waves a SIMD: one workgroup of eight waves a CU, or two of four)
+__global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockGemmArgs a) {
+  constexpr int WAVES = WM * WN, BM = 16 * MG * WM, BN = 16 * NG * WN;
+  constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;   // direct loads per wave and step, eight rows each
+  static_assert(XI * 8 * WAVES == BM && WI * 8 * WAVES == BN, "the waves share the staged rows evenly");
+  constexpr int SR = BM / WAVES, SP = SR + 4;               // rows whose scales a wave loads; its place for them
+  constexpr int XB = BM * kStepBytes, WB = BN * kStepBytes;
+  constexpr int STAGE = XB + WB + (T::kScaled ? WAVES * SP * 4 : 0);
+  constexpr int LOADS = XI + WI + (T::kScaled ? 1 : 0);
+  constexpr int SPREAD = kStages > 2 && MG > 2 ? MG - 1 : (MG > 2 ? 2 : 1);  // row groups over which the loads are spread
+  static_assert(kStages * STAGE >= WAVES * 16 * (32 * NG + 16), "the epilogue's staging fits");
+  __shared__ __attribute__((aligned(128))) uint8_t smem[kStages * STAGE];
   __shared__ int s_slot[BM];
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wm = w / WN, wn = w % WN;
 
-  const int strips = (a.N + 64 * NG - 1) / (64 * NG), subs = (a.block_m + BM - 1) / BM;
+  const int strips = (a.N + BN - 1) / BN, subs = (a.block_m + BM - 1) / BM;
   int mb, strip;
-  grouped_block(strips, a.group_m, mb, strip);
-  const int b = mb / subs, sub = mb - b * subs;
-  int e = 0;
-  if (a.sorted) {
-    if ((int64_t)b * a.block_m >= *a.ntpp) return;
-    e = a.eids[b];
-    if (e < 0 || e >= a.E) return;
+  unit_tile(blockIdx.x, strips, a.group_m, a.group_n, mb, strip);
+  if (mb >= a.tiles || strip >= strips) return;
+  int b = mb / subs, e = 0;
+  const int sub = kMerge ? 0 : mb - b * subs;
+  int rows = min(a.block_m - sub * BM, BM);
+  if constexpr (kMerge) {
+    rows = merged_tile(a, a.cap_blocks, BM, mb, reinterpret_cast<int*>(smem), &b);
+    if (rows == 0) return;
+    __syncthreads();  // (the blocks' experts have been read: the first loads may take their place)
   }
-  if (tid < BM) s_slot[tid] = slot_of(a, b, sub * BM + tid);
-  __syncthreads();
-  const int lg = live_groups<BM>(s_slot, lane);
-  if (lg == 0) return;  // (uniform over the workgroup)
+  // A workgroup is alone on its CU, so its start is not hidden: everything that says what it works on
+  // is asked for at once (entries behind the live blocks exist, so no load waits for the block count)
+  // and the first steps' operands before the tile's rows are counted.
+  const int64_t first = (int64_t)b * a.block_m + sub * BM;
+  int xs[XI], ss = -1;
+#pragma unroll
+  for (int l = 0; l < XI; ++l) {
+    const int r = (w * XI + l) * 8 + (lane >> 3);
+    xs[l] = r < rows ? slot_at(a, first + r) : -1;
+  }
+  if (T::kScaled && lane % SR + w * SR < rows) ss = slot_at(a, first + w * SR + lane % SR);
+  if (a.sorted) {
+    const int nb = *a.ntpp / a.block_m;
+    e = a.eids[b];
+    if (b >= nb || e < 0 || e >= a.E) return;
+  }
 
   const int KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   const bool ragged = a.Kb % kStepBytes != 0;
-  const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
+  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;  // (a load's rows start at a multiple of eight)
 
-  // activations: load l of wave w is operand half i of group g, i * MG + g = 4 l + w
-  const uint8_t* xp[XL];
+  const uint8_t* xp[XI];
 #pragma unroll
-  for (int l = 0; l < XL; ++l) {
-    const int i = (4 * l + w) / MG, g = (4 * l + w) % MG;
-    const int s = s_slot[g * 16 + (lane & 15)];
-    xp[l] = a.A + (int64_t)(s >= 0 ? s / a.top_k : 0) * a.lda + i * 64 + 16 * (lane >> 4);
-  }
-  // scales of the rows, staged [row % 16][group]
-  const uint8_t* sp = nullptr;
-  if constexpr (T::kScaled) {
-    const int p = (w * 64 + lane) % BM, s = s_slot[(p % MG) * 16 + p / MG];
-    sp = reinterpret_cast<const uint8_t*>(a.sa + (int64_t)(s >= 0 ? s / a.top_k : 0) * a.ld_sa);
-  }
-  auto issue_x = [&](auto partial, int kt, int stage) __attribute__((always_inline)) {
+  for (int l = 0; l < XI; ++l) xp[l] = a.A + (int64_t)(xs[l] >= 0 ? xs[l] / a.top_k : 0) * a.lda + piece;
+  const int nw = strip * BN;  // the strip's weight rows (clamped at the N edge, not stored)
+  const uint8_t* wbase = uniform_ptr(a.W + ((int64_t)e * a.N + nw) * a.Kb);
+  uint32_t woff[WI];
+#pragma unroll
+  for (int l = 0; l < WI; ++l)
+    woff[l] = (uint32_t)min((w * WI + l) * 8 + (lane >> 3), a.N - 1 - nw) * (uint32_t)a.Kb + (uint32_t)piece;
+  const int n0 = nw + wn * 16 * NG;
+  // scales: lane l < SR brings that of row w * SR + l, lane SR that of the wave's own weight rows (16 NG
+  // rows from a multiple of 16 NG lie in one block of 128).  All of it by direct loads: an ordinary
+  // load in the loop would be waited for with every direct load in flight.
+  const float* sp = nullptr;
+  if constexpr (T::kScaled)
+    sp = lane < SR ? a.sa + (int64_t)(ss >= 0 ? ss / a.top_k : 0) * a.ld_sa
+                   : a.sb + ((int64_t)e * ((a.N + kScaleBlock - 1) / kScaleBlock) + min(n0, a.N - 1) / kScaleBlock) * KT;
+  int lg = 0;  // (set below)
+  // Loads first .. last - 1 of step kt's (past the end the last step's again, not used: every step has the
+  // same count of loads).
+  auto issue = [&](int kt, int stage, int first, int last) __attribute__((always_inline)) {
     const uint32_t st = smem_lds + (uint32_t)(stage * STAGE);
-    const bool tail = ragged && kt == KT - 1;
-#pragma unroll
-    for (int l = 0; l < XL; ++l) {
-      const int i = (4 * l + w) / MG, g = (4 * l + w) % MG;
-      if (decltype(partial)::value && g >= lg) continue;  // all padding: never read
-      const uint8_t* p = xp[l] + (int64_t)kt * kStepBytes;
-      if (tail && kt * kStepBytes + i * 64 + 16 * (lane >> 4) >= a.Kb) p = zero;
-      dma_from<16>(p, st + (uint32_t)(4 * l + w) * 1024);
-    }
-    if constexpr (T::kScaled) {
-      if (w * 64 < BM) {
-        if (BM >= 64 || lane < BM) dma_from<4>(sp + (int64_t)kt * 4, st + XB + (uint32_t)(w * 256));
-      }
-    }
-  };
-  // weights: rows n0 .. n0 + 16 NG - 1 of the expert (clamped at the N edge, not stored)
-  const int n0 = (strip * 4 + w) * 16 * NG;
-  const int nbase = min(n0, a.N - 1);
-  const uint8_t* wbase = uniform_ptr(a.W + ((int64_t)e * a.N + nbase) * a.Kb);
-  uint32_t woff[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g)
-    woff[g] = (uint32_t)(min(n0 + g * 16 + (lane & 15), a.N - 1) - nbase) * (uint32_t)a.Kb + 16u * (lane >> 4);
-  auto load_w = [&](int kt, Frag (&f)[NG]) __attribute__((always_inline)) {
-    const uint8_t* p = wbase + (int64_t)kt * kStepBytes;
+    kt = min(kt, KT - 1);
+    auto load = [&](int l) __attribute__((always_inline)) {
+      if (l < XI) dma_from<16>(xp[l] + (int64_t)kt * kStepBytes, st + (uint32_t)(w * XI + l) * 1024);
+      else dma_to_lds<16>(wbase + (int64_t)kt * kStepBytes, woff[l - XI], st + XB + (uint32_t)(w * WI + l - XI) * 1024);
+    };
     if (ragged && kt == KT - 1) {
-      const int k = kt * kStepBytes + 16 * (lane >> 4);
+      // What lies behind K is zero in both operands (a NaN pattern there must not meet a zero); a load
+      // has lanes in front of it in any case.
+      const bool in = kt * kStepBytes + piece < a.Kb;
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        f[g] = load_frag(k < a.Kb ? p + woff[g] : zero, k + 64 < a.Kb ? p + woff[g] + 64 : zero);
+      for (int l = 0; l < XI + WI; ++l) {
+        if (l < first || l >= last) continue;
+        uint8_t* place = smem + stage * STAGE + (l < XI ? (w * XI + l) * 1024 : XB + (w * WI + l - XI) * 1024) + lane * 16;
+        if (in) load(l);
+        else *reinterpret_cast<u32x4_t*>(place) = u32x4_t{0u, 0u, 0u, 0u};
+      }
     } else {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) f[g] = load_frag(p + woff[g], p + woff[g] + 64);
+      for (int l = 0; l < XI + WI; ++l)
+        if (l >= first && l < last) load(l);
+    }
+    if constexpr (T::kScaled) {
+      if (last == LOADS && lane <= SR)
+        dma_from<4>(reinterpret_cast<const uint8_t*>(sp + kt), st + XB + WB + (uint32_t)(w * SP) * 4);
     }
   };
-  const float* sbp = nullptr;
-  if constexpr (T::kScaled)  // (16 NG rows from a multiple of 16 NG: one block of 128)
-    sbp = a.sb + ((int64_t)e * ((a.N + kScaleBlock - 1) / kScaleBlock) + nbase / kScaleBlock) * KT;
 
   f32x4_t acc[NG][MG];
 #pragma unroll
@@ -370,94 +452,132 @@ __global__ __launch_bounds__(256, 2) void block_gemm_tile_kernel(BlockGemmArgs a
 #pragma unroll
     for (int h = 0; h < MG; ++h) acc[g][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+  // the operand of the 16 staged rows at `rows`
+  const int lo = (lane & 15) * kStepBytes + (((lane >> 4) ^ (lane & 7)) * 16);
+  const int hi = (lane & 15) * kStepBytes + (((4 + (lane >> 4)) ^ (lane & 7)) * 16);
+  auto read = [&](const uint8_t* rows) __attribute__((always_inline)) { return load_frag(rows + lo, rows + hi); };
   auto read_x = [&](const uint8_t* st, int h) __attribute__((always_inline)) {
-    return load_frag(st + h * 1024 + lane * 16, st + (MG + h) * 1024 + lane * 16);
+    return read(st + (h * WM + wm) * 16 * kStepBytes);
   };
   auto read_s = [&](const uint8_t* st, int h) __attribute__((always_inline)) {
-    return T::kScaled ? reinterpret_cast<const float*>(st + XB)[(lane & 15) * MG + h] : 0.f;
+    const int r = (h * WM + wm) * 16 + (lane & 15);
+    return T::kScaled ? reinterpret_cast<const float*>(st + XB + WB)[r / SR * SP + r % SR] : 0.f;
   };
-  // One step's products.  An expert's last block (PARTIAL) skips its all-padding groups.
-  auto compute = [&](auto partial, const uint8_t* st, const Frag (&wf)[NG], float sb) __attribute__((always_inline)) {
+  auto read_sb = [&](const uint8_t* st) __attribute__((always_inline)) {
+    return T::kScaled ? reinterpret_cast<const float*>(st + XB + WB)[w * SP + SR] : 0.f;
+  };
+  auto read_w = [&](const uint8_t* st, int g) __attribute__((always_inline)) {
+    return read(st + XB + (wn * NG + g) * 16 * kStepBytes);
+  };
+  // A product of e4m3fn operands is scaled into the sum DIST products later, across row groups and steps,
+  // so that one wave keeps the matrix core and the vector unit busy together and does not stand
+  // for the product's latency (16 passes).  acc += t * s for the product before the last DIST:
+  constexpr int DIST = !T::kScaled ? 1 : (NG * MG > 16 || NG * MG < 4 ? 2 : 4);
+  f32x4_t t[DIST];
+  float ts[DIST];
+#pragma unroll
+  for (int i = 0; i < DIST; ++i) {
+    t[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    ts[i] = 0.f;
+  }
+  auto take = [&](int i, const f32x4_t& v, float s) __attribute__((always_inline)) {  // i: number of the product
+    f32x4_t& c = acc[i % NG][i / NG];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = fmaf(v[q], s, c[q]);
+    asm volatile("" : "+v"(c));  // taken here: the compiler else sinks it into later blocks
+  };
+  constexpr int P = NG * MG;  // products of a step
+  static_assert(P % DIST == 0, "a step ends where the ring of products began");
+  Frag wf[NG], x0;            // this step's weights, and its first row group
+  float s0 = 0.f, sb = 0.f;   // scales: of that row group, of the weights
+  // Products of row group h; where `next` is given (the last group of a step) each weight tile's place
+  // takes the next step's behind its last product.
+  auto products = [&](auto partial, const Frag& x, float s, int h, const uint8_t* next) __attribute__((always_inline)) {
     constexpr bool PARTIAL = decltype(partial)::value;
     if constexpr (T::kScaled) {
-      // The scaled sum of a product is taken two MFMAs after it, so that one wave keeps the matrix
-      // core and the vector unit busy together; the scheduling barriers hold that order (left to
-      // itself the compiler gathers the products first, which spills).
-      f32x4_t t[3];
-      float sv[3];
-      auto take = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i % NG][i / NG][q] = fmaf(t[i % 3][q], sv[i % 3], acc[i % NG][i / NG][q]);
-        asm volatile("" : "+v"(acc[i % NG][i / NG]));  // taken here (not sunk into the next step's blocks)
-      };
-      Frag x = read_x(st, 0);
-      float sc = read_s(st, 0);
-#pragma unroll
-      for (int h = 0; h < MG; ++h) {
-        if (PARTIAL && h >= lg) continue;
-        const Frag xn = h + 1 < MG ? read_x(st, h + 1) : x;
-        const float sn = h + 1 < MG ? read_s(st, h + 1) : 0.f;
-        const float s = sc * sb;
+      if constexpr (!PARTIAL) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const int i = h * NG + g;
-          t[i % 3] = mfma_step(T{}, wf[g], x);
-          sv[i % 3] = s;
-          if (PARTIAL ? g >= 2 : i >= 2) take(i - 2);
+          const f32x4_t now = mfma_step(T{}, wf[g], x);
+          __builtin_amdgcn_sched_barrier(0);
+          if (next) wf[g] = read_w(next, g);
+          take((i + P - DIST) % P, t[i % DIST], ts[i % DIST]);
+          t[i % DIST] = now;
+          ts[i % DIST] = s;
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (PARTIAL || h + 1 == MG) {
-          take(h * NG + NG - 2);
-          take(h * NG + NG - 1);
-        }
-        x = xn;
-        sc = sn;
-      }
-    } else {
+        return;
+      } else if (h < lg) {  // (an expert's last tile: each group for itself)
+        f32x4_t v[NG];
 #pragma unroll
-      for (int h = 0; h < MG; ++h) {
-        if (PARTIAL && h >= lg) continue;
-        const Frag x = read_x(st, h);
+        for (int g = 0; g < NG; ++g) v[g] = mfma_step(T{}, wf[g], x);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) acc[g][h] = mfma_step(T{}, wf[g], x, acc[g][h]);
+        for (int g = 0; g < NG; ++g) take(h * NG + g, v[g], s);
       }
+    } else if (!PARTIAL || h < lg) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) acc[g][h] = mfma_step(T{}, wf[g], x, acc[g][h]);
+    }
+    if (next) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) wf[g] = read_w(next, g);
     }
   };
-
-  // One step: the next step's operands are requested first (the weights before the direct loads, so
-  // that the wait the compiler puts before a weight's first use counts nothing but weights), and
-  // have all landed when the step's closing barrier is passed.
-  Frag wa[NG], wb[NG];
-  float sba = 0.f, sbb = 0.f;
-  auto landed = [&](Frag (&f)[NG]) __attribute__((always_inline)) {
-    wait_vm<0>();
+  auto step = [&](auto partial, int kt, int stage) __attribute__((always_inline)) {
+    const uint8_t* st = smem + stage * STAGE;
+    const uint8_t* next = smem + (stage + 1 == kStages ? 0 : stage + 1) * STAGE;
+    const int target = stage == 0 ? kStages - 1 : stage - 1;
+    Frag x = x0;
+    float s = s0;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) asm volatile("" : "+v"(f[g]));
+    for (int h = 0; h + 1 < MG; ++h) {
+      // the loads are spread over the row groups: a wave that issues them all at once waits for the
+      // address unit, which takes 16 clocks for each and is shared by the CU
+      if (h < SPREAD) issue(kt + kStages - 1, target, LOADS * h / SPREAD, LOADS * (h + 1) / SPREAD);
+      const Frag xn = read_x(st, h + 1);
+      const float sn = read_s(st, h + 1);
+      products(partial, x, s * sb, h, nullptr);
+      x = xn;
+      s = sn;
+    }
+    wait_vm<(kStages - 2) * LOADS>();
     block_barrier();
-  };
-  auto step = [&](auto partial, int kt, int stage, const Frag (&cur)[NG], Frag (&next)[NG], float sc,
-                  float& sn) __attribute__((always_inline)) {
-    const int kn = min(kt + 1, KT - 1);  // (past the end the last step again, not used)
-    load_w(kn, next);
-    if constexpr (T::kScaled) sn = sbp[kn];
-    issue_x(partial, kn, stage ^ 1);
-    compute(partial, smem + stage * STAGE, cur, sc);
-    landed(next);
+    x0 = read_x(next, 0);
+    s0 = read_s(next, 0);
+    const float sbn = read_sb(next);
+    products(partial, x, s * sb, MG - 1, next);
+    sb = sbn;
   };
   auto k_loop = [&](auto partial) __attribute__((always_inline)) {
-    int kt = 0;
-    for (; kt + 1 < KT; kt += 2) {
-      step(partial, kt, 0, wa, wb, sba, sbb);
-      step(partial, kt + 1, 1, wb, wa, sbb, sba);
+    for (int kt = 0, stage = 0; kt < KT; ++kt) {
+      step(partial, kt, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    if (kt < KT) step(partial, kt, 0, wa, wb, sba, sbb);
   };
-  load_w(0, wa);
-  if constexpr (T::kScaled) sba = sbp[0];
-  issue_x(std::true_type{}, 0, 0);
-  landed(wa);
-  if (lg == MG) k_loop(std::false_type{});
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s, s, 0, LOADS);
+  if (tid < BM) s_slot[tid] = tid < rows ? slot_at(a, first + tid) : -1;
+  wait_vm<0>();  // (the first steps: the slots' load stands behind them)
+  block_barrier();
+  const int live = live_groups<BM>(s_slot, lane);
+  // The 16-row groups go to the WM wave rows in turn, so that they share a partly filled tile evenly: of
+  // this wave's groups h (group h * WM + wm of the tile) the first lg are live.
+  lg = (live - wm + WM - 1) / WM;
+  if (live == 0) return;  // (uniform over the workgroup, and nothing is in flight)
+#pragma unroll
+  for (int g = 0; g < NG; ++g) wf[g] = read_w(smem, g);
+  x0 = read_x(smem, 0);
+  s0 = read_s(smem, 0);
+  sb = read_sb(smem);
+  if (lg >= MG) k_loop(std::false_type{});
   else k_loop(std::true_type{});
+  if constexpr (T::kScaled) {
+#pragma unroll
+    for (int i = P - DIST; i < P; ++i) take(i, t[i % DIST], ts[i % DIST]);
+  }
+  wait_vm<0>();     // the loads past the end have landed and every wave has read its last operands:
+  block_barrier();  // the stages are free for the epilogue
 
   if (a.bias) {
 #pragma unroll
@@ -471,32 +591,78 @@ __global__ __launch_bounds__(256, 2) void block_gemm_tile_kernel(BlockGemmArgs a
     }
   }
   const bool wide = ((uintptr_t)a.C & 15) == 0 && (a.ldc & 7) == 0;
-  store_tiles<NG, MG, uint16_t>(acc, lg, smem, SMEM, w, lane, n0, a.N, wide, [&](int r) -> uint16_t* {
-    const int s = s_slot[r];
+  store_tiles<NG, MG, uint16_t>(acc, lg, smem, w, lane, n0, a.N, wide, [&](int r) -> uint16_t* {
+    const int s = s_slot[((r >> 4) * WM + wm) * 16 + (r & 15)];
     return s >= 0 ? a.C + (int64_t)s * a.ldc : nullptr;
   });
 }
 
-template <typename T, int MG>
+template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge = false>
 static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipStream_t st) {
-  constexpr int NG = 4;
-  a.group_m = default_group_m(a.Kb / T::kBytes, a.block_m);
-  const int64_t grid = (int64_t)((a.N + 64 * NG - 1) / (64 * NG)) * cap_blocks * ((a.block_m + 16 * MG - 1) / (16 * MG));
-  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-  hipLaunchKernelGGL((block_gemm_tile_kernel<T, MG, NG>), dim3((unsigned)grid), dim3(256), 0, st, a);
+  constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
+  a.cap_blocks = (int32_t)cap_blocks;
+  int64_t tiles = cap_blocks * ((a.block_m + BM - 1) / BM);
+  if (kMerge) {  // an expert's last tile may hold fewer blocks
+    const int64_t per = BM / a.block_m, experts = std::min<int64_t>(a.E, a.numel);
+    tiles = std::min(cap_blocks, (cap_blocks + experts * (per - 1)) / per);
+  }
+  // Units of 4 x 8, a workgroup for each CU of an XCD, or smaller ones where there are not eight of them.
+  // (Measured on the Zipf prefill product: units of 1 x all strips, 2 x 16 and 4 x 8 1076, 1024, 999 us;
+  // units that take all strips leave some XCDs a quarter of the tiles more than others.)
+  const int64_t strips = (a.N + BN - 1) / BN, unit = std::min<int64_t>(32, std::max<int64_t>(1, tiles * strips / kXcds));
+  a.group_m = (int32_t)std::min<int64_t>({4, tiles, unit});
+  a.group_n = (int32_t)std::min<int64_t>(strips, std::max<int64_t>(1, unit / a.group_m));
+  a.tiles = (int32_t)tiles;
+  const int64_t units = (tiles + a.group_m - 1) / a.group_m * ((strips + a.group_n - 1) / a.group_n);
+  const int64_t grid = (units + kXcds - 1) / kXcds * kXcds * a.group_m * a.group_n;
+  MOE_REQUIRE(grid < (1ll << 31) && tiles < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+  hipLaunchKernelGGL((block_gemm_tile_kernel<T, MG, NG, WM, WN, kStages, kMerge>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, st, a);
   return check_launch(fn);
 }
 
+// The kernel for a call.  Blocks of at most 16 rows stream their weights (block_gemm_stream_kernel).  For
+// the others the tile with the least rounds x time of a step (one step of 128 bytes of K of all the
+// workgroups that are resident, measured for e4m3fn; bf16's have the same proportions):
+//   256 x 256, one workgroup a CU: 1.87 us     128 x 256, one a CU: 1.08 us
+//   128 x 128, two a CU: 1.17 us                64 x 64, two a CU: 0.45 us
+// Blocks of at most 64 rows have no use for the larger ones: 64 x 256 or 32 x 256, and 64 x 64 where
+// these leave CUs without work.  256-row tiles are made of an expert's 128-row blocks, counted in the
+// kernel, where the batch has 512 slots an expert (fewer leave its last, partly filled tile too large a
+// share: 1024 tokens of 8 choices on 32 local experts 614 us with 128 rows, 655 with 256).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
-  if (a.block_m > 64) return launch_tile<T, 8>(fn, a, cap_blocks, st);
-  if (a.block_m > 32) return launch_tile<T, 4>(fn, a, cap_blocks, st);
-  if (a.block_m > 16) return launch_tile<T, 2>(fn, a, cap_blocks, st);
-  constexpr int NG = 2, KS = 4;
-  const int64_t grid = (int64_t)((a.N + 16 * NG - 1) / (16 * NG)) * cap_blocks;
-  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-  hipLaunchKernelGGL((block_gemm_stream_kernel<T, NG, KS>), dim3((unsigned)grid), dim3(64 * KS), 0, st, a);
-  return check_launch(fn);
+  if (a.block_m <= 16) {
+    constexpr int NG = 2, KS = 4;
+    const int64_t grid = (int64_t)((a.N + 16 * NG - 1) / (16 * NG)) * cap_blocks;
+    MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+    hipLaunchKernelGGL((block_gemm_stream_kernel<T, NG, KS>), dim3((unsigned)grid), dim3(64 * KS), 0, st, a);
+    return check_launch(fn);
+  }
+  const int64_t cus = device_cu_count();
+  auto count = [&](int BM, int BN) { return cap_blocks * ((a.block_m + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
+  if (a.block_m <= 32) {
+    if (count(32, 256) < cus) return launch_tile<T, 2, 1, 1, 4, 4>(fn, a, cap_blocks, st);
+    return launch_tile<T, 2, 4, 1, 4, 2>(fn, a, cap_blocks, st);
+  }
+  if (a.block_m <= 64) {
+    if (count(64, 256) < cus) return launch_tile<T, 2, 2, 2, 2, 4>(fn, a, cap_blocks, st);
+    return launch_tile<T, 2, 4, 2, 4, 3>(fn, a, cap_blocks, st);
+  }
+  constexpr int64_t kMaxMerged = 16384;  // blocks whose experts fit the kernel's LDS
+  const bool merge = a.sorted && a.block_m == 128 && cap_blocks <= kMaxMerged && a.numel >= 512ll * a.E;
+  auto rounds = [&](int64_t n, int per_cu) { return (double)((n + cus * per_cu - 1) / (cus * per_cu)); };
+  const double big = merge ? rounds((count(128, 256) + 1) / 2, 1) * 1.87
+                           : (a.sorted && a.block_m <= 128 ? 1e30 : rounds(count(256, 256), 1) * 1.87);
+  const double mid = rounds(count(128, 256), 1) * 1.08, low = rounds(count(128, 128), 2) * 1.17;
+  const double small = rounds(count(64, 64), 2) * 0.45;
+  if (big <= std::min({mid, low, small})) {
+    if (merge) return launch_tile<T, 8, 4, 2, 4, 2, true>(fn, a, cap_blocks, st);
+    return launch_tile<T, 8, 4, 2, 4, 2>(fn, a, cap_blocks, st);
+  }
+  if (mid <= std::min(low, small)) return launch_tile<T, 4, 4, 2, 4, 3>(fn, a, cap_blocks, st);
+  if (low <= small) return launch_tile<T, 4, 4, 2, 2, 2>(fn, a, cap_blocks, st);
+  return launch_tile<T, 2, 2, 2, 2, 4>(fn, a, cap_blocks, st);
 }
 
 // Checks shared by the products over the align's blocks (A and W of T::kBytes a value).
@@ -507,8 +673,8 @@ static int check_block_gemm(const char* fn, const void* A, int64_t a_rows, int64
   constexpr int kStep = 16 / T::kBytes;
   MOE_REQUIRE(E >= 1 && N >= 1 && K >= 1, MOE_EINVAL, "%s: E=%d N=%d K=%d", fn, E, N, K);
   MOE_REQUIRE(E <= 512, MOE_EUNSUPPORTED, "%s: %d experts (at most 512)", fn, E);
-  MOE_REQUIRE(N % 8 == 0 && K % kStep == 0 && N <= (1 << 24) && K <= (1 << 24), MOE_EUNSUPPORTED,
-              "%s: N=%d must be a multiple of 8 and K=%d of %d (both at most 2^24)", fn, N, K, kStep);
+  MOE_REQUIRE(N % 8 == 0 && K % kStep == 0 && N <= (1 << 20) && K <= (1 << 20), MOE_EUNSUPPORTED,
+              "%s: N=%d must be a multiple of 8 and K=%d of %d (both at most 2^20)", fn, N, K, kStep);
   MOE_REQUIRE(numel >= 0 && top_k >= 1 && block_m >= 1 && block_m <= 256, MOE_EINVAL,
               "%s: numel=%lld top_k=%d block_m=%d (1..256)", fn, (long long)numel, top_k, block_m);
   MOE_REQUIRE(numel < (1 << 30), MOE_EUNSUPPORTED, "%s: numel=%lld", fn, (long long)numel);

@@ -22,7 +22,7 @@ static int w8a8(const char* fn, bool dense, const uint8_t* A, int64_t a_rows, in
     if (rc) return rc;
   }
   const BlockGemmArgs a{A, lda, W, a_scales, ld_as, w_scales, bias, C, ldc, dense ? nullptr : sorted, eids, ntpp,
-                        (int32_t)numel, top_k, block_m, N, K, E, 0};
+                        (int32_t)numel, top_k, block_m, N, K, E, 0, 0, 0, 0};
   return launch_block_gemm<Fp8Type>(fn, a, cap_blocks, stream);
 }
 
@@ -39,5 +39,5 @@ extern "C" int moe_w8a8_linear(const uint8_t* A, int64_t M, int64_t lda, const f
                                const uint8_t* W, const float* w_scales, const uint16_t* bias, int32_t N, int32_t K,
                                uint16_t* C, int64_t ldc, hipStream_t stream) {
   return w8a8("moe_w8a8_linear", true, A, M, lda, a_scales, ld_scales, W, w_scales, bias, 1, N, K, C, ldc, nullptr,
-              nullptr, nullptr, M, 1, M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)), stream);
+              nullptr, nullptr, M, 1, M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 256)), stream);
 }

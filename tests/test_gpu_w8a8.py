@@ -47,6 +47,16 @@ def test_shapes(M, k, E, N, K, B, gather):
     case(M, k, E, E, N, K, B, k if gather else 1, M % 2 == 1, M + N + K)
 
 
+@pytest.mark.parametrize("M,k,E,N,K,B", [(1100, 1, 2, 520, 400, 128), (2100, 2, 8, 264, 272, 128), (700, 2, 2, 1032, 256, 256),
+                                         (5000, 1, 3, 2056, 144, 128), (4200, 1, 1, 4104, 128, 128)])
+def test_tiles_of_several_blocks(M, k, E, N, K, B):
+    # enough slots an expert for 256-row tiles, made of two 128-row blocks or of one of 256; skewed, so
+    # that experts end inside a tile, in its first block, or have no slot
+    r = np.random.default_rng(M)
+    case(M, k, 2 * E, E, N, K, B, k, True, M, only=r.choice(2 * E, size=max(k, E), replace=False))
+    case(M, k, E, E, N, K, B, 1, False, M + 1, only=[E - 1] if k == 1 else None)
+
+
 @pytest.mark.parametrize("B", [16, 64, 128])
 def test_slice_strides_and_what_lies_behind_rows(B):
     # a slice of the experts (most slots dropped), rows of A and of the output apart with NaN codes
