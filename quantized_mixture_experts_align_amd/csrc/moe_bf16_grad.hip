@@ -3,9 +3,9 @@
 //   moe_bf16_gemm_wgrad   dW[e, n, k] = sum over the slots s of e of dC[s, n] A[s / top_k, k]
 //                         dbias[e, n] = sum over the slots s of e of dC[s, n]
 // Both products reduce over an index whose values are rows in memory (n of W; the slots of dC and
-// A), while an MFMA operand wants eight consecutive values of it in one lane.  The tiles are staged
-// in LDS as they lie in memory and read with ds_read_b64_tr_b16: within 16 lanes that together read
-// four rows of 16 values, lane i receives column i.
+// A), while an MFMA operand wants eight consecutive values of it in one lane: the tiles are staged
+// in LDS as they lie in memory and read transposed (moe_block_gemm.h, which also holds the kernel of
+// the first one: the product with the weights as the transposed operand).
 //
 // Sums run in fp32 in a fixed order (no atomics).
 #include <algorithm>
@@ -17,98 +17,30 @@ namespace moe {
 struct GradArgs {
   const uint16_t* dC;
   int64_t ld_dc;
-  const uint16_t* A;   // wgrad
+  const uint16_t* A;
   int64_t lda;
-  const uint16_t* W;   // dgrad: [E, N, K]
-  void* dX;            // dgrad: a row for each slot (bf16, or fp32 to be summed over a row's slots)
-  int64_t ld_dx;
-  void* dW;            // wgrad: [E, N, K]
-  void* dbias;         // wgrad: [E, N] or null
+  void* dW;            // [E, N, K]
+  void* dbias;         // [E, N] or null
   const int32_t* sorted;
   const int32_t* eids;
   const int32_t* ntpp;
   int32_t numel, top_k, block_m, N, K, E;
+  int32_t cap_blocks;  // most blocks the align can have made
+  int32_t group_m, group_n;
+  uint32_t div_mul, div_shift;  // s / top_k for 0 <= s < 2^31 (top_k > 1)
+  __device__ __forceinline__ uint32_t row_of(uint32_t s) const {
+    return top_k == 1 ? s : __umulhi(s, div_mul) >> div_shift;
+  }
 };
-
-typedef __attribute__((ext_vector_type(4))) int16_t s16x4_t;
-
-// Lane i of each 16-lane group reads 8 bytes at its own address; it receives the i-th value of each
-// of the four rows that lanes 0-3, 4-7, 8-11 and 12-15 hold.
-__device__ __forceinline__ u32x2_t lds_read_tr(const uint8_t* p) {
-  const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
-  return __builtin_bit_cast(u32x2_t, v);
-}
-
-// The transposed operand of 16 columns at byte column `col` of a staged tile [32][pitch bytes]:
-// lane l gets column l % 16, rows 8 (l / 16) + 0..7.
-__device__ __forceinline__ u32x4_t tr_frag(const uint8_t* tile, int pitch, int col, int lane) {
-  const uint8_t* p = tile + (8 * (lane >> 4) + ((lane & 15) >> 2)) * pitch + col + (lane & 3) * 8;
-  const u32x2_t lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * pitch);
-  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-}
-
-// dX[s, k] of 64 slots of a block x 64 columns k: wave w holds columns 16 w .. 16 w + 15.
-template <typename OUT>
-__global__ __launch_bounds__(256) void dgrad_kernel(GradArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t ws[32 * 128];     // 32 rows n x 64 columns k
-  __shared__ __attribute__((aligned(16))) uint8_t cs[64 * 64];      // 64 slots x 32 columns n
-  __shared__ int s_slot[64];
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
-  const int strips = (a.K + 63) / 64, subs = (a.block_m + 63) / 64;
-  const int strip = blockIdx.x % strips, rest = blockIdx.x / strips;
-  const int b = rest / subs, sub = rest - b * subs;
-  if ((int64_t)b * a.block_m >= *a.ntpp) return;
-  const int e = a.eids[b];
-  if (e < 0 || e >= a.E) return;
-  if (tid < 64) {
-    const int p = sub * 64 + tid;
-    const int s = p < a.block_m ? a.sorted[(int64_t)b * a.block_m + p] : -1;
-    s_slot[tid] = s >= 0 && s < a.numel ? s : -1;
-  }
-  __syncthreads();
-  f32x4_t acc[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) acc[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int n0 = 0; n0 < a.N; n0 += 32) {
-    {
-      const int r = tid >> 3, k = strip * 64 + (tid & 7) * 8;   // 32 rows x 8 chunks of 8 columns
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (n0 + r < a.N && k < a.K) v = *reinterpret_cast<const u32x4_t*>(a.W + ((int64_t)e * a.N + n0 + r) * a.K + k);
-      *reinterpret_cast<u32x4_t*>(ws + r * 128 + (tid & 7) * 16) = v;
-      const int q = tid >> 2, n = n0 + (tid & 3) * 8, s = s_slot[q];  // 64 slots x 4 chunks
-      u32x4_t c = {0u, 0u, 0u, 0u};
-      if (s >= 0 && n < a.N) c = *reinterpret_cast<const u32x4_t*>(a.dC + (int64_t)s * a.ld_dc + n);
-      *reinterpret_cast<u32x4_t*>(cs + q * 64 + (tid & 3) * 16) = c;
-    }
-    __syncthreads();
-    const u32x4_t wf = tr_frag(ws, 128, w * 32, lane);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const u32x4_t cf = *reinterpret_cast<const u32x4_t*>(cs + (h * 16 + (lane & 15)) * 64 + (lane >> 4) * 16);
-      acc[h] = mfma(wf, cf, acc[h]);
-    }
-    __syncthreads();
-  }
-  const int k0 = strip * 64 + w * 16 + 4 * (lane >> 4);
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int s = s_slot[h * 16 + (lane & 15)];
-    if (s < 0 || k0 >= a.K) continue;
-    OUT* o = static_cast<OUT*>(a.dX) + (int64_t)s * a.ld_dx + k0;
-    if constexpr (sizeof(OUT) == 4) *reinterpret_cast<f32x4_t*>(o) = acc[h];
-    else *reinterpret_cast<u32x2_t*>(o) = u32x2_t{pack_bf16x2(acc[h][0], acc[h][1]), pack_bf16x2(acc[h][2], acc[h][3])};
-  }
-}
 
 // [first, last) of the sorted entries of expert e: the align lists the experts' blocks in rising
 // order, so counting the live blocks of lower and of equal experts gives its range.  Every thread
 // of the workgroup calls it; `red` holds two ints for each wave.
-__device__ __forceinline__ void expert_range(const int32_t* eids, const int32_t* ntpp, int block_m, int e, int* red,
-                                             int64_t* first, int64_t* last) {
-  const int nb = *ntpp / block_m, lane = threadIdx.x & 63;
+__device__ __forceinline__ void expert_range(const GradArgs& a, int e, int* red, int64_t* first, int64_t* last) {
+  const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), lane = threadIdx.x & 63;
   int lower = 0, equal = 0;
   for (int i = threadIdx.x; i < nb; i += blockDim.x) {
-    const int v = eids[i];
+    const int v = a.eids[i];
     lower += v < e;
     equal += v == e;
   }
@@ -126,50 +58,148 @@ __device__ __forceinline__ void expert_range(const int32_t* eids, const int32_t*
     lower += red[2 * i];
     equal += red[2 * i + 1];
   }
-  *first = (int64_t)lower * block_m;
-  *last = *first + (int64_t)equal * block_m;
+  *first = (int64_t)lower * a.block_m;
+  *last = *first + (int64_t)equal * a.block_m;
 }
 
-// dW[e, n, k] of 64 rows n x 64 columns k: wave w holds columns 16 w .. 16 w + 15.
-template <typename OUT>
-__global__ __launch_bounds__(256) void wgrad_kernel(GradArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t xs[32 * 128];  // 32 slots x 64 columns k of A
-  __shared__ __attribute__((aligned(16))) uint8_t cs[32 * 128];  // 32 slots x 64 columns n of dC
-  __shared__ int red[8];
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
-  const int ks = (a.K + 63) / 64, ns = (a.N + 63) / 64;
-  const int kt = blockIdx.x % ks, rest = blockIdx.x / ks, nt = rest % ns, e = rest / ns;
+// dW[e, n, k] of BM = 16 * MG * WM rows n x BN = 16 * NG * WN columns k, reduced over the expert's slots in
+// steps of 64: the slots' rows of dC (BM columns of each) and of A (BN columns) go through LDS as they lie
+// in memory, kStages steps deep, and both operands are read transposed.  Wave (wm, wn) owns MG 16-row
+// groups of n and NG 16-column tiles of k.
+//
+// The rows are gathered, so a step's loads need its slots' numbers: each wave loads the 64 numbers of a
+// step for itself, by a direct load into its own ring in LDS, early enough that they have landed (by the
+// wait that lets step kt run) when the rows of that step are asked for.  An expert's slots fill its
+// blocks from the front, so only its last step can lack rows; they are zero in both operands.
+template <typename OUT, int MG, int NG, int WM, int WN, int kStages>
+__global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
+  constexpr int WAVES = WM * WN, BM = 16 * MG * WM, BN = 16 * NG * WN, ROWS = 64;
+  constexpr int PC = BM * 2, PX = BN * 2;                       // bytes of a staged row of dC and of A
+  constexpr int CI = ROWS * PC / 1024 / WAVES, XI = ROWS * PX / 1024 / WAVES;  // loads per wave and step
+  constexpr int RC = 1024 / PC, RX = 1024 / PX;                 // rows that a load brings
+  static_assert(CI * 1024 * WAVES == ROWS * PC && XI * 1024 * WAVES == ROWS * PX, "the waves share the rows evenly");
+  constexpr int CB = ROWS * PC, STAGE = CB + ROWS * PX, LOADS = CI + XI + 1;
+  constexpr int RING = 2 * kStages;                             // steps whose slot numbers are held
+  static_assert(kStages * STAGE >= WAVES * 16 * (32 * NG + 16), "the epilogue's staging fits");
+  __shared__ __attribute__((aligned(128))) uint8_t smem[kStages * STAGE];
+  __shared__ __attribute__((aligned(16))) int s_ids[WAVES][RING][ROWS];
+  __shared__ int red[2 * WAVES];
+  const uint32_t smem_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const uint32_t ids_lds =
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int*)&s_ids[0][0][0] + (uint32_t)w * RING * ROWS * 4;
+  const int wm = w / WN, wn = w % WN;
+  const int ks = (a.K + BN - 1) / BN, ns = (a.N + BM - 1) / BM;
+  int en, kt0;
+  unit_tile(blockIdx.x, ks, a.group_m, a.group_n, en, kt0);
+  if (kt0 >= ks || en >= ns * a.E) return;
+  const int e = en / ns, nt = en - e * ns;
   int64_t first, last;
-  expert_range(a.eids, a.ntpp, a.block_m, e, red, &first, &last);
-  f32x4_t acc[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) acc[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int r = tid >> 3, c8 = (tid & 7) * 8;
-  for (int64_t p = first; p < last; p += 32) {
-    const int s = p + r < last ? a.sorted[p + r] : -1;
-    const bool live = s >= 0 && s < a.numel;
-    u32x4_t x = {0u, 0u, 0u, 0u}, c = x;
-    if (live && kt * 64 + c8 < a.K)
-      x = *reinterpret_cast<const u32x4_t*>(a.A + (int64_t)(s / a.top_k) * a.lda + kt * 64 + c8);
-    if (live && nt * 64 + c8 < a.N)
-      c = *reinterpret_cast<const u32x4_t*>(a.dC + (int64_t)s * a.ld_dc + nt * 64 + c8);
-    *reinterpret_cast<u32x4_t*>(xs + r * 128 + c8 * 2) = x;
-    *reinterpret_cast<u32x4_t*>(cs + r * 128 + c8 * 2) = c;
-    __syncthreads();
-    const u32x4_t xf = tr_frag(xs, 128, w * 32, lane);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) acc[h] = mfma(xf, tr_frag(cs, 128, h * 32, lane), acc[h]);
-    __syncthreads();
+  expert_range(a, e, red, &first, &last);
+  int rows = 0;  // the expert's slots
+  if (last > first) {
+    const int64_t tail = last - a.block_m;
+    int live = 0;
+    for (int i = lane; i < a.block_m; i += 64) {
+      const int s = a.sorted[tail + i];
+      live += s >= 0 && s < a.numel;
+    }
+    for (int d = 32; d >= 1; d >>= 1) live += __shfl_xor(live, d);
+    rows = __builtin_amdgcn_readfirstlane((int)(tail - first) + live);
   }
-  const int k0 = kt * 64 + w * 16 + 4 * (lane >> 4);
+  const int KT = (rows + ROWS - 1) / ROWS;
+  const int n0 = nt * BM, k0 = kt0 * BN;
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
+
+  int crow[CI], xrow[XI];
+  uint32_t ccol[CI], xcol[XI];  // byte offsets in a row (a column behind the edge reads the first, not stored)
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int n = nt * 64 + h * 16 + (lane & 15);
-    if (n >= a.N || k0 >= a.K) continue;
-    OUT* o = static_cast<OUT*>(a.dW) + ((int64_t)e * a.N + n) * a.K + k0;
-    if constexpr (sizeof(OUT) == 4) *reinterpret_cast<f32x4_t*>(o) = acc[h];
-    else *reinterpret_cast<u32x2_t*>(o) = u32x2_t{pack_bf16x2(acc[h][0], acc[h][1]), pack_bf16x2(acc[h][2], acc[h][3])};
+  for (int l = 0; l < CI; ++l) {
+    crow[l] = (w * CI + l) * RC + lane / (64 / RC);
+    const int place = lane % (64 / RC), col = n0 + ((place >> 1) ^ trans_swizzle(crow[l], PC)) * 16 + (place & 1) * 8;
+    ccol[l] = 2u * (uint32_t)(col < a.N ? col : n0);
   }
+#pragma unroll
+  for (int l = 0; l < XI; ++l) {
+    xrow[l] = (w * XI + l) * RX + lane / (64 / RX);
+    const int place = lane % (64 / RX), col = k0 + ((place >> 1) ^ trans_swizzle(xrow[l], PX)) * 16 + (place & 1) * 8;
+    xcol[l] = 2u * (uint32_t)(col < a.K ? col : k0);
+  }
+  // the slot numbers of step kt (behind the last row: the last one's again)
+  auto issue_ids = [&](int kt) __attribute__((always_inline)) {
+    const int64_t at = first + min(kt * ROWS + lane, rows - 1);
+    dma_from<4>(reinterpret_cast<const uint8_t*>(a.sorted + at), ids_lds + (uint32_t)(kt % RING) * ROWS * 4);
+  };
+  auto issue = [&](int kt, int stage, int from, int to) __attribute__((always_inline)) {
+    const uint32_t st = smem_lds + (uint32_t)(stage * STAGE);
+    kt = min(kt, KT - 1);
+    const int* ids = s_ids[w][kt % RING];
+    const int left = rows - kt * ROWS;
+#pragma unroll
+    for (int l = 0; l < CI + XI; ++l) {
+      if (l < from || l >= to) continue;
+      const int r = l < CI ? crow[l] : xrow[l - CI];
+      const uint32_t s = min((uint32_t)ids[r], (uint32_t)(a.numel - 1));
+      const uint8_t* p;
+      if (l < CI) p = reinterpret_cast<const uint8_t*>(a.dC) + (int64_t)s * (a.ld_dc * 2) + ccol[l];
+      else p = reinterpret_cast<const uint8_t*>(a.A) + (int64_t)a.row_of(s) * (a.lda * 2) + xcol[l - CI];
+      dma_from<16>(r < left ? p : zero,
+                   st + (l < CI ? (uint32_t)(w * CI + l) * 1024 : CB + (uint32_t)(w * XI + l - CI) * 1024));
+    }
+  };
+
+  f32x4_t acc[NG][MG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int h = 0; h < MG; ++h) acc[g][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (KT > 0) {
+    int coff[MG], xoff[NG];
+#pragma unroll
+    for (int h = 0; h < MG; ++h) coff[h] = trans_lane(wm * MG + h, PC, lane);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) xoff[g] = trans_lane(wn * NG + g, PX, lane);
+    // Step j asks for the rows of step j + kStages - 1 and the numbers of step j + 2 (kStages - 1).
+#pragma unroll
+    for (int s = 0; s < 2 * (kStages - 1); ++s) issue_ids(s);
+    wait_vm<0>();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) issue(s, s, 0, CI + XI);
+    wait_vm<(kStages - 2) * (CI + XI)>();
+    block_barrier();
+    u32x4_t xf[2][NG];
+    auto read_x = [&](const uint8_t* st, int sub, int g) __attribute__((always_inline)) {
+      return trans_operand(st + CB + sub * 32 * PX, xoff[g], PX);
+    };
+    for (int kt = 0, stage = 0; kt < KT; ++kt) {
+      const uint8_t* st = smem + stage * STAGE;
+      const int target = stage == 0 ? kStages - 1 : stage - 1;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) xf[sub][g] = read_x(st, sub, g);
+#pragma unroll
+      for (int h = 0; h < MG; ++h) {
+        if (h < 2) issue(kt + kStages - 1, target, (CI + XI) * h / 2, (CI + XI) * (h + 1) / 2);
+        if (h == 1) issue_ids(kt + 2 * (kStages - 1));
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const u32x4_t cf = trans_operand(st + sub * 32 * PC, coff[h], PC);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) acc[g][h] = mfma(xf[sub][g], cf, acc[g][h]);
+        }
+      }
+      wait_vm<(kStages - 2) * LOADS>();
+      block_barrier();
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    wait_vm<0>();
+    block_barrier();
+  }
+  store_tiles<NG, MG, OUT>(acc, MG, smem, w, lane, k0 + wn * 16 * NG, a.K, true, [&](int r) -> OUT* {
+    const int n = n0 + wm * 16 * MG + r;
+    return n < a.N ? static_cast<OUT*>(a.dW) + ((int64_t)e * a.N + n) * a.K : nullptr;
+  });
 }
 
 // dbias[e, n] of 128 columns: 16 chunks of eight columns x 16 rows at a time, joined in row order.
@@ -180,7 +210,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(GradArgs a) {
   const int tid = threadIdx.x, r = tid >> 4, c8 = (tid & 15) * 8;
   const int ns = (a.N + 127) / 128, nt = blockIdx.x % ns, e = blockIdx.x / ns;
   int64_t first, last;
-  expert_range(a.eids, a.ntpp, a.block_m, e, red, &first, &last);
+  expert_range(a, e, red, &first, &last);
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -230,6 +260,20 @@ __global__ __launch_bounds__(256) void zero_dead_kernel(const int32_t* __restric
     for (int c = threadIdx.x * 8; c < K; c += 256 * 8)
       *reinterpret_cast<u32x4_t*>(dst + r * ld + c) = u32x4_t{0u, 0u, 0u, 0u};
   }
+}
+
+template <typename OUT>
+static int launch_wgrad(const char* fn, GradArgs a, hipStream_t st) {
+  constexpr int MG = 4, NG = 4, WM = 2, WN = 4, BM = 16 * MG * WM, BN = 16 * NG * WN;
+  const int64_t tiles = (int64_t)((a.N + BM - 1) / BM) * a.E, strips = (a.K + BN - 1) / BN;
+  const int64_t unit = std::min<int64_t>(32, std::max<int64_t>(1, tiles * strips / kXcds));
+  a.group_m = (int32_t)std::min<int64_t>({4, tiles, unit});
+  a.group_n = (int32_t)std::min<int64_t>(strips, std::max<int64_t>(1, unit / a.group_m));
+  const int64_t units = (tiles + a.group_m - 1) / a.group_m * ((strips + a.group_n - 1) / a.group_n);
+  const int64_t grid = (units + kXcds - 1) / kXcds * kXcds * a.group_m * a.group_n;
+  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+  hipLaunchKernelGGL((wgrad_kernel<OUT, MG, NG, WM, WN, 3>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, st, a);
+  return check_launch(fn);
 }
 
 static int zero_dead(const char* fn, const int32_t* live, int64_t rows, int32_t K, uint16_t* dst, int64_t ld,
@@ -293,13 +337,12 @@ extern "C" int moe_bf16_gemm_dgrad(const uint16_t* dC, int64_t ld_dc, const uint
   int64_t cap = 0, cap_blocks = 0;
   rc = moe_align_capacity(numel, 1, E, block_m, &cap, &cap_blocks);
   if (rc) return rc;
-  const GradArgs a{dC, ld_dc, nullptr, 0, W, top_k == 1 ? static_cast<void*>(dA) : work, top_k == 1 ? ld_da : (int64_t)K, nullptr, nullptr,
-                   sorted_token_ids, expert_ids, num_tokens_post_padded, (int32_t)numel, top_k, block_m, N, K, E};
-  const int64_t grid = (int64_t)((K + 63) / 64) * cap_blocks * ((block_m + 63) / 64);
-  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-  if (top_k == 1) hipLaunchKernelGGL(dgrad_kernel<uint16_t>, dim3((unsigned)grid), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL(dgrad_kernel<float>, dim3((unsigned)grid), dim3(256), 0, stream, a);
-  rc = check_launch(fn);
+  const BlockGemmArgs a{reinterpret_cast<const uint8_t*>(dC), ld_dc * 2, reinterpret_cast<const uint8_t*>(W), nullptr,
+                        0, nullptr, nullptr, top_k == 1 ? static_cast<void*>(dA) : work,
+                        top_k == 1 ? ld_da : (int64_t)K, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                        (int32_t)numel, 1, block_m, K, N * 2, E, 0, 0, 0, 0};
+  rc = top_k == 1 ? launch_block_gemm<Bf16TransType<uint16_t>>(fn, a, cap_blocks, stream)
+                  : launch_block_gemm<Bf16TransType<float>>(fn, a, cap_blocks, stream);
   if (rc) return rc;
   if (top_k == 1) return zero_dead(fn, slot_local_ids, numel, K, dA, ld_da, stream);
   hipLaunchKernelGGL(sum_slots_kernel, dim3((unsigned)(numel / top_k)), dim3(256), 0, stream, work,
@@ -322,13 +365,16 @@ extern "C" int moe_bf16_gemm_wgrad(const uint16_t* dC, int64_t ld_dc, const uint
               "%s: null pointer", fn);
   MOE_REQUIRE((((uintptr_t)A | (uintptr_t)dW) & 15) == 0 && ((uintptr_t)dbias & 3) == 0, MOE_EUNSUPPORTED,
               "%s: misaligned pointer (A and dW 16 B, dbias 4 B)", fn);
-  const GradArgs a{dC, ld_dc, A, lda, nullptr, nullptr, 0, dW, dbias, sorted_token_ids, expert_ids,
-                   num_tokens_post_padded, (int32_t)numel, top_k, block_m, N, K, E};
-  const int64_t grid = (int64_t)((K + 63) / 64) * ((N + 63) / 64) * E;
-  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-  if (out_f32) hipLaunchKernelGGL(wgrad_kernel<float>, dim3((unsigned)grid), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL(wgrad_kernel<uint16_t>, dim3((unsigned)grid), dim3(256), 0, stream, a);
-  rc = check_launch(fn);
+  int64_t cap = 0, cap_blocks = 0;
+  rc = moe_align_capacity(numel, 1, E, block_m, &cap, &cap_blocks);
+  if (rc) return rc;
+  GradArgs a{dC, ld_dc, A, lda, dW, dbias, sorted_token_ids, expert_ids, num_tokens_post_padded, (int32_t)numel, top_k,
+             block_m, N, K, E, (int32_t)cap_blocks, 0, 0, 0, 0};
+  if (top_k > 1) {  // ceil(2^(32 + shift) / top_k): exact for numerators below 2^31
+    while ((2u << a.div_shift) < (uint32_t)top_k) ++a.div_shift;
+    a.div_mul = (uint32_t)(((1ull << (32 + a.div_shift)) + top_k - 1) / (uint64_t)top_k);
+  }
+  rc = out_f32 ? launch_wgrad<float>(fn, a, stream) : launch_wgrad<uint16_t>(fn, a, stream);
   if (rc || !dbias) return rc;
   const unsigned gb = (unsigned)((int64_t)((N + 127) / 128) * E);
   if (out_f32) hipLaunchKernelGGL(bias_grad_kernel<float>, dim3(gb), dim3(256), 0, stream, a);

@@ -29,7 +29,7 @@ struct BlockGemmArgs {
   int64_t ld_sa;
   const float* sb;        // e4m3fn: [E, ceil(N / 128), ceil(K / 128)]
   const uint16_t* bias;   // bf16 [E, N] or null
-  uint16_t* C;
+  void* C;
   int64_t ldc;
   const int32_t* sorted;  // null: dense, block b holds rows b * block_m ..., expert 0
   const int32_t* eids;
@@ -40,12 +40,21 @@ struct BlockGemmArgs {
 };
 
 struct Fp8Type {
-  static constexpr bool kScaled = true;
+  static constexpr bool kScaled = true, kTrans = false;
   static constexpr int kBytes = 1;
+  typedef uint16_t Out;
 };
 struct Bf16Type {
-  static constexpr bool kScaled = false;
+  static constexpr bool kScaled = false, kTrans = false;
   static constexpr int kBytes = 2;
+  typedef uint16_t Out;
+};
+// The product's gradient: the reduction runs over the rows of W, C[s, n] = sum_k A[s, k] W[e, k, n] with
+// W [E, Kb / 2, N] (N: the columns of C).  OUT: bf16 or fp32 rows.
+template <typename OUT>
+struct Bf16TransType : Bf16Type {
+  static constexpr bool kTrans = true;
+  typedef OUT Out;
 };
 
 typedef __attribute__((ext_vector_type(4))) int32_t i32x4_t;
@@ -73,7 +82,7 @@ __device__ __forceinline__ Frag load_frag(const uint8_t* lo, const uint8_t* hi) 
 static __device__ const u32x4_t g_zero16 = {0u, 0u, 0u, 0u};
 
 // acc + the step's product (bf16), or the step's product alone (e4m3fn, scaled by the caller)
-__device__ __forceinline__ f32x4_t mfma_step(Bf16Type, const Frag& w, const Frag& x, f32x4_t acc) {
+__device__ __forceinline__ f32x4_t mfma_step(const Bf16Type&, const Frag& w, const Frag& x, f32x4_t acc) {
   acc = mfma(frag_lo(w), frag_lo(x), acc);
   return mfma(frag_hi(w), frag_hi(x), acc);
 }
@@ -180,7 +189,7 @@ __global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArg
         const u32x2_t bb = *reinterpret_cast<const u32x2_t*>(a.bias + (int64_t)e * a.N + n0);
         v[0] += bf16_lo(bb[0]); v[1] += bf16_hi(bb[0]); v[2] += bf16_lo(bb[1]); v[3] += bf16_hi(bb[1]);
       }
-      *reinterpret_cast<u32x2_t*>(a.C + (int64_t)slot * a.ldc + n0) =
+      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.C) + (int64_t)slot * a.ldc + n0) =
           u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
   }
@@ -274,6 +283,35 @@ __device__ __forceinline__ void dma_from(const uint8_t* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(p) : "memory", "m0");
 }
 
+// ---------------------------------------------------------------------------- transposed operands
+// A tile whose rows are the reduction index, as it lies in memory, staged [rows][16 bytes * kPieces] with
+// the pairs of 16-byte pieces of a row (16 values) at place pair ^ trans_swizzle(row).  An operand of 16
+// columns is read with ds_read_b64_tr_b16: within 16 lanes that together read four rows of 16 values,
+// lane i receives column i, so two of them give a lane the eight consecutive rows that an MFMA wants.
+// The swizzle keeps the rows that 32 lanes read together, 8 j + r for j = 0, 1 and r = 0..3, in
+// different banks (rows of 128 bytes have four pairs, and two rows then share a bank).
+__device__ __forceinline__ int trans_swizzle(int row, int pitch) {
+  return ((row & 3) | ((row >> 1) & 4)) & (pitch / 32 - 1);
+}
+
+typedef __attribute__((ext_vector_type(4))) int16_t s16x4_t;
+__device__ __forceinline__ u32x2_t lds_read_tr(const uint8_t* p) {
+  const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+  return __builtin_bit_cast(u32x2_t, v);
+}
+// Where lane l begins to read pair `pair` of the staged rows: row 8 (l / 16) + (l % 16) / 4, the lane's
+// 8 bytes of the pair.  (The swizzle is the same for that row plus 4 and plus any multiple of 16.)
+__device__ __forceinline__ int trans_lane(int pair, int pitch, int lane) {
+  const int row = 8 * (lane >> 4) + ((lane & 15) >> 2);
+  return row * pitch + ((pair ^ trans_swizzle(row, pitch)) << 5) + (lane & 3) * 8;
+}
+// The operand of 32 rows from `tile` on.
+__device__ __forceinline__ u32x4_t trans_operand(const uint8_t* tile, int lane_off, int pitch) {
+  const u32x2_t lo = lds_read_tr(tile + lane_off), hi = lds_read_tr(tile + lane_off + 4 * pitch);
+  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// ---------------------------------------------------------------------------- blocks of rows, the kernel
 // Launch index -> (tile of rows, strip of weight rows).  A unit of group_m tiles x group_n strips runs
 // on one XCD, so that its workgroups share activations and weights in that XCD's L2; the units go
 // round the XCDs, strips first, so that the eight that run side by side share tiles of rows.
@@ -395,17 +433,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
 
   const int KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   const bool ragged = a.Kb % kStepBytes != 0;
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
   const int piece = ((lane & 7) ^ (lane >> 3)) * 16;  // (a load's rows start at a multiple of eight)
 
   const uint8_t* xp[XI];
 #pragma unroll
   for (int l = 0; l < XI; ++l) xp[l] = a.A + (int64_t)(xs[l] >= 0 ? xs[l] / a.top_k : 0) * a.lda + piece;
-  const int nw = strip * BN;  // the strip's weight rows (clamped at the N edge, not stored)
-  const uint8_t* wbase = uniform_ptr(a.W + ((int64_t)e * a.N + nw) * a.Kb);
+  const int nw = strip * BN;  // the strip's weight rows, or columns (clamped at the N edge, not stored)
+  // Trans: 64 rows of the reduction a step, PW bytes of each; a load brings RW of them
+  constexpr int PW = BN * 2, RW = 1024 / PW;
+  const int64_t wpitch = T::kTrans ? (int64_t)a.N * 2 : a.Kb;
+  const uint8_t* wbase = uniform_ptr(T::kTrans ? a.W + (int64_t)e * (a.Kb / 2) * wpitch + nw * 2
+                                               : a.W + ((int64_t)e * a.N + nw) * a.Kb);
+  const int64_t wstep = T::kTrans ? (kStepBytes / 2) * wpitch : kStepBytes;
   uint32_t woff[WI];
+  int wrow[WI];  // Trans: the row of the reduction that this lane loads
 #pragma unroll
-  for (int l = 0; l < WI; ++l)
-    woff[l] = (uint32_t)min((w * WI + l) * 8 + (lane >> 3), a.N - 1 - nw) * (uint32_t)a.Kb + (uint32_t)piece;
+  for (int l = 0; l < WI; ++l) {
+    if constexpr (T::kTrans) {
+      wrow[l] = (w * WI + l) * RW + lane / (64 / RW);
+      const int place = lane % (64 / RW), col = ((place >> 1) ^ trans_swizzle(wrow[l], PW)) * 16 + (place & 1) * 8;
+      woff[l] = (uint32_t)(wrow[l] * wpitch) + (nw + col < a.N ? (uint32_t)col * 2 : 0u);
+    } else {
+      woff[l] = (uint32_t)min((w * WI + l) * 8 + (lane >> 3), a.N - 1 - nw) * (uint32_t)a.Kb + (uint32_t)piece;
+    }
+  }
   const int n0 = nw + wn * 16 * NG;
   // scales: lane l < SR brings that of row w * SR + l, lane SR that of the wave's own weight rows (16 NG
   // rows from a multiple of 16 NG lie in one block of 128).  All of it by direct loads: an ordinary
@@ -422,18 +474,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
     kt = min(kt, KT - 1);
     auto load = [&](int l) __attribute__((always_inline)) {
       if (l < XI) dma_from<16>(xp[l] + (int64_t)kt * kStepBytes, st + (uint32_t)(w * XI + l) * 1024);
-      else dma_to_lds<16>(wbase + (int64_t)kt * kStepBytes, woff[l - XI], st + XB + (uint32_t)(w * WI + l - XI) * 1024);
+      else dma_to_lds<16>(wbase + kt * wstep, woff[l - XI], st + XB + (uint32_t)(w * WI + l - XI) * 1024);
     };
     if (ragged && kt == KT - 1) {
-      // What lies behind K is zero in both operands (a NaN pattern there must not meet a zero); a load
-      // has lanes in front of it in any case.
-      const bool in = kt * kStepBytes + piece < a.Kb;
+      // What lies behind K is zero in both operands (a NaN pattern there must not meet a zero).
+      const bool in_row = kt * kStepBytes + piece < a.Kb;
 #pragma unroll
       for (int l = 0; l < XI + WI; ++l) {
         if (l < first || l >= last) continue;
-        uint8_t* place = smem + stage * STAGE + (l < XI ? (w * XI + l) * 1024 : XB + (w * WI + l - XI) * 1024) + lane * 16;
-        if (in) load(l);
-        else *reinterpret_cast<u32x4_t*>(place) = u32x4_t{0u, 0u, 0u, 0u};
+        const uint8_t* p = l < XI ? xp[l] + (int64_t)kt * kStepBytes : wbase + kt * wstep + woff[l - XI];
+        const bool in = T::kTrans && l >= XI ? kt * (kStepBytes / 2) + wrow[l - XI] < a.Kb / 2 : in_row;
+        dma_from<16>(in ? p : zero,
+                     st + (l < XI ? (uint32_t)(w * XI + l) * 1024 : XB + (uint32_t)(w * WI + l - XI) * 1024));
       }
     } else {
 #pragma unroll
@@ -453,6 +505,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
     for (int h = 0; h < MG; ++h) acc[g][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   // the operand of the 16 staged rows at `rows`
+  int trans_off[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) trans_off[g] = trans_lane(wn * NG + g, PW, lane);
   const int lo = (lane & 15) * kStepBytes + (((lane >> 4) ^ (lane & 7)) * 16);
   const int hi = (lane & 15) * kStepBytes + (((4 + (lane >> 4)) ^ (lane & 7)) * 16);
   auto read = [&](const uint8_t* rows) __attribute__((always_inline)) { return load_frag(rows + lo, rows + hi); };
@@ -467,7 +522,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
     return T::kScaled ? reinterpret_cast<const float*>(st + XB + WB)[w * SP + SR] : 0.f;
   };
   auto read_w = [&](const uint8_t* st, int g) __attribute__((always_inline)) {
-    return read(st + XB + (wn * NG + g) * 16 * kStepBytes);
+    if constexpr (T::kTrans)
+      return frag_of(trans_operand(st + XB, trans_off[g], PW), trans_operand(st + XB + 32 * PW, trans_off[g], PW));
+    else
+      return read(st + XB + (wn * NG + g) * 16 * kStepBytes);
   };
   // A product of e4m3fn operands is scaled into the sum DIST products later, across row groups and steps,
   // so that one wave keeps the matrix core and the vector unit busy together and does not stand
@@ -590,10 +648,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
       for (int h = 0; h < MG; ++h) acc[g][h] += bv;
     }
   }
+  typedef typename T::Out Out;
   const bool wide = ((uintptr_t)a.C & 15) == 0 && (a.ldc & 7) == 0;
-  store_tiles<NG, MG, uint16_t>(acc, lg, smem, w, lane, n0, a.N, wide, [&](int r) -> uint16_t* {
+  store_tiles<NG, MG, Out>(acc, lg, smem, w, lane, n0, a.N, wide, [&](int r) -> Out* {
     const int s = s_slot[((r >> 4) * WM + wm) * 16 + (r & 15)];
-    return s >= 0 ? a.C + (int64_t)s * a.ldc : nullptr;
+    return s >= 0 ? static_cast<Out*>(a.C) + (int64_t)s * a.ldc : nullptr;
   });
 }
 
@@ -632,7 +691,7 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
 // share: 1024 tokens of 8 choices on 32 local experts 614 us with 128 rows, 655 with 256).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
-  if (a.block_m <= 16) {
+  if constexpr (!T::kTrans) if (a.block_m <= 16) {
     constexpr int NG = 2, KS = 4;
     const int64_t grid = (int64_t)((a.N + 16 * NG - 1) / (16 * NG)) * cap_blocks;
     MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
