@@ -34,14 +34,14 @@ struct GradArgs {
 };
 
 // [first, last) of the sorted entries of expert e: the align lists the experts' blocks in rising
-// order, so counting the live blocks of lower and of equal experts gives its range.  Every thread
-// of the workgroup calls it; `red` holds two ints for each wave.
+// order (and -1 behind them), so counting the blocks of lower and of equal experts gives its range.
+// Every thread of the workgroup calls it; `red` holds two ints for each wave.
 __device__ __forceinline__ void expert_range(const GradArgs& a, int e, int* red, int64_t* first, int64_t* last) {
-  const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
   int lower = 0, equal = 0;
-  for (int i = threadIdx.x; i < nb; i += blockDim.x) {
+  for (int i = threadIdx.x; i < a.cap_blocks; i += blockDim.x) {
     const int v = a.eids[i];
-    lower += v < e;
+    lower += v >= 0 && v < e;
     equal += v == e;
   }
   for (int d = 32; d >= 1; d >>= 1) {
@@ -96,16 +96,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
   const int e = en / ns, nt = en - e * ns;
   int64_t first, last;
   expert_range(a, e, red, &first, &last);
+  // the slot numbers of step kt (behind the last entry the last one again)
+  auto issue_ids = [&](int kt) __attribute__((always_inline)) {
+    const int64_t at = min(first + (int64_t)kt * ROWS + lane, last - 1);
+    dma_from<4>(reinterpret_cast<const uint8_t*>(a.sorted + at), ids_lds + (uint32_t)(kt % RING) * ROWS * 4);
+  };
   int rows = 0;  // the expert's slots
   if (last > first) {
+#pragma unroll
+    for (int s = 0; s < 2 * (kStages - 1); ++s) issue_ids(s);
     const int64_t tail = last - a.block_m;
-    int live = 0;
-    for (int i = lane; i < a.block_m; i += 64) {
-      const int s = a.sorted[tail + i];
-      live += s >= 0 && s < a.numel;
+    rows = (int)(tail - first);
+    for (int i = 0; i < a.block_m; i += 64) {
+      const int s = i + lane < a.block_m ? a.sorted[tail + i + lane] : -1;
+      rows += __popcll(__ballot(s >= 0 && s < a.numel));
     }
-    for (int d = 32; d >= 1; d >>= 1) live += __shfl_xor(live, d);
-    rows = __builtin_amdgcn_readfirstlane((int)(tail - first) + live);
+    rows = __builtin_amdgcn_readfirstlane(rows);
   }
   const int KT = (rows + ROWS - 1) / ROWS;
   const int n0 = nt * BM, k0 = kt0 * BN;
@@ -125,11 +131,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
     const int place = lane % (64 / RX), col = k0 + ((place >> 1) ^ trans_swizzle(xrow[l], PX)) * 16 + (place & 1) * 8;
     xcol[l] = 2u * (uint32_t)(col < a.K ? col : k0);
   }
-  // the slot numbers of step kt (behind the last row: the last one's again)
-  auto issue_ids = [&](int kt) __attribute__((always_inline)) {
-    const int64_t at = first + min(kt * ROWS + lane, rows - 1);
-    dma_from<4>(reinterpret_cast<const uint8_t*>(a.sorted + at), ids_lds + (uint32_t)(kt % RING) * ROWS * 4);
-  };
   auto issue = [&](int kt, int stage, int from, int to) __attribute__((always_inline)) {
     const uint32_t st = smem_lds + (uint32_t)(stage * STAGE);
     kt = min(kt, KT - 1);
@@ -160,37 +161,54 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) xoff[g] = trans_lane(wn * NG + g, PX, lane);
     // Step j asks for the rows of step j + kStages - 1 and the numbers of step j + 2 (kStages - 1).
-#pragma unroll
-    for (int s = 0; s < 2 * (kStages - 1); ++s) issue_ids(s);
     wait_vm<0>();
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue(s, s, 0, CI + XI);
     wait_vm<(kStages - 2) * (CI + XI)>();
     block_barrier();
-    u32x4_t xf[2][NG];
+    u32x4_t xf[2][NG], cf[2];
     auto read_x = [&](const uint8_t* st, int sub, int g) __attribute__((always_inline)) {
       return trans_operand(st + CB + sub * 32 * PX, xoff[g], PX);
     };
+    auto read_c = [&](const uint8_t* st, int sub, int h) __attribute__((always_inline)) {
+      return trans_operand(st + sub * 32 * PC, coff[h], PC);
+    };
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) xf[sub][g] = read_x(smem, sub, g);
+      cf[sub] = read_c(smem, sub, 0);
+    }
     for (int kt = 0, stage = 0; kt < KT; ++kt) {
       const uint8_t* st = smem + stage * STAGE;
+      const uint8_t* next = smem + (stage + 1 == kStages ? 0 : stage + 1) * STAGE;
       const int target = stage == 0 ? kStages - 1 : stage - 1;
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) xf[sub][g] = read_x(st, sub, g);
-#pragma unroll
       for (int h = 0; h < MG; ++h) {
-        if (h < 2) issue(kt + kStages - 1, target, (CI + XI) * h / 2, (CI + XI) * (h + 1) / 2);
-        if (h == 1) issue_ids(kt + 2 * (kStages - 1));
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const u32x4_t cf = trans_operand(st + sub * 32 * PC, coff[h], PC);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) acc[g][h] = mfma(xf[sub][g], cf, acc[g][h]);
+        u32x4_t cn[2];
+        if (h + 1 < MG) {
+          if (h < 2) issue(kt + kStages - 1, target, (CI + XI) * h / 2, (CI + XI) * (h + 1) / 2);
+          if (h == 1) issue_ids(kt + 2 * (kStages - 1));
+          cn[0] = read_c(st, 0, h + 1);
+          cn[1] = read_c(st, 1, h + 1);
+        } else {  // the next step's operands are read behind the last group's products
+          wait_vm<(kStages - 2) * LOADS>();
+          block_barrier();
+          cn[0] = read_c(next, 0, 0);
+          cn[1] = read_c(next, 1, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            acc[g][h] = mfma(xf[sub][g], cf[sub], acc[g][h]);
+            if (h + 1 == MG) xf[sub][g] = read_x(next, sub, g);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+        cf[0] = cn[0];
+        cf[1] = cn[1];
       }
-      wait_vm<(kStages - 2) * LOADS>();
-      block_barrier();
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     wait_vm<0>();
@@ -215,15 +233,21 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(GradArgs a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
   const int n = nt * 128 + c8;
-  for (int64_t p = first + r; p < last; p += 16) {
-    const int s = a.sorted[p];
-    if (s < 0 || s >= a.numel || n >= a.N) continue;
-    const u32x4_t c = *reinterpret_cast<const u32x4_t*>(a.dC + (int64_t)s * a.ld_dc + n);
+  for (int64_t p = first + r; p < last; p += 16 * 8) {  // eight rows in flight a thread
+    u32x4_t c[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] += bf16_lo(c[j]);
-      v[2 * j + 1] += bf16_hi(c[j]);
+    for (int u = 0; u < 8; ++u) {
+      const int s = p + 16 * u < last ? a.sorted[p + 16 * u] : -1;
+      c[u] = u32x4_t{0u, 0u, 0u, 0u};
+      if (s >= 0 && s < a.numel && n < a.N) c[u] = *reinterpret_cast<const u32x4_t*>(a.dC + (int64_t)s * a.ld_dc + n);
     }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] += bf16_lo(c[u][j]);
+        v[2 * j + 1] += bf16_hi(c[u][j]);
+      }
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) part[r][c8 + j] = v[j];
@@ -262,9 +286,9 @@ __global__ __launch_bounds__(256) void zero_dead_kernel(const int32_t* __restric
   }
 }
 
-template <typename OUT>
-static int launch_wgrad(const char* fn, GradArgs a, hipStream_t st) {
-  constexpr int MG = 4, NG = 4, WM = 2, WN = 4, BM = 16 * MG * WM, BN = 16 * NG * WN;
+template <typename OUT, int MG, int NG, int WM, int WN, int kStages>
+static int launch_wgrad_tile(const char* fn, GradArgs a, hipStream_t st) {
+  constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
   const int64_t tiles = (int64_t)((a.N + BM - 1) / BM) * a.E, strips = (a.K + BN - 1) / BN;
   const int64_t unit = std::min<int64_t>(32, std::max<int64_t>(1, tiles * strips / kXcds));
   a.group_m = (int32_t)std::min<int64_t>({4, tiles, unit});
@@ -272,8 +296,17 @@ static int launch_wgrad(const char* fn, GradArgs a, hipStream_t st) {
   const int64_t units = (tiles + a.group_m - 1) / a.group_m * ((strips + a.group_n - 1) / a.group_n);
   const int64_t grid = (units + kXcds - 1) / kXcds * kXcds * a.group_m * a.group_n;
   MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-  hipLaunchKernelGGL((wgrad_kernel<OUT, MG, NG, WM, WN, 3>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, st, a);
+  hipLaunchKernelGGL((wgrad_kernel<OUT, MG, NG, WM, WN, kStages>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, st, a);
   return check_launch(fn);
+}
+
+// 256 x 256 tiles (8192 slots on 8 experts, N = K = 4096: 317 us; 128 x 256 417, 128 x 128 405), or 128 x 128
+// where these leave CUs without work (4608 slots on 8 experts, N = 2048, K = 512: 28.5 and 20.9 us).
+template <typename OUT>
+static int launch_wgrad(const char* fn, const GradArgs& a, hipStream_t st) {
+  if ((int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E >= device_cu_count())
+    return launch_wgrad_tile<OUT, 8, 4, 2, 4, 2>(fn, a, st);
+  return launch_wgrad_tile<OUT, 4, 2, 2, 4, 2>(fn, a, st);
 }
 
 static int zero_dead(const char* fn, const int32_t* live, int64_t rows, int32_t K, uint16_t* dst, int64_t ld,

@@ -100,34 +100,53 @@ __device__ __forceinline__ int slot_at(const BlockGemmArgs& a, int64_t at) {
 }
 
 // ---------------------------------------------------------------------------- few rows
-// Workgroup = 16 slots of a block x NG 16-row weight tiles, K split over its KS waves, operands
-// straight from memory to registers in chunks of kChunk steps, partial sums joined through LDS in
-// wave order.  For blocks of at most 16 slots the cost is the stream of weights, of which each
-// wave has NG * 2 * kChunk 16-byte loads a lane in flight.
-template <typename T, int NG, int KS>
+// Workgroup = up to 16 slots of a block (MB = 2: of two consecutive blocks of one expert) x NG 16-row
+// weight tiles, K split over its KS waves, operands straight from memory to registers in chunks of
+// kChunk steps, partial sums joined through LDS in wave order.  The cost is the stream of weights (64 tokens of 8 choices on 32 of 256
+// experts, N = 8192, K = 4096: 139 us, 6.7 TB/s).
+template <typename T, int NG, int KS, int MB>
 __global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArgs a) {
   constexpr int kChunk = 4;
-  __shared__ f32x4_t part[KS][NG][64];
+  __shared__ f32x4_t part[KS][NG * MB][64];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int strips = (a.N + 16 * NG - 1) / (16 * NG);
   const int strip = blockIdx.x % strips, b = blockIdx.x / strips;
-  int e = 0;
+  int e = 0, blocks = 1;
   if (a.sorted) {
-    if ((int64_t)b * a.block_m >= *a.ntpp) return;
     e = a.eids[b];
-    if (e < 0 || e >= a.E) return;
+    if constexpr (MB == 2) {
+      // the expert's blocks in front of b, and whether the next one is its too
+      const int next = b + 1 < a.cap_blocks ? a.eids[b + 1] : -1;
+      int before = 0;
+      for (;;) {
+        const int i = b - 1 - before - lane;
+        const uint64_t other = __ballot(i < 0 || a.eids[i < 0 ? 0 : i] != e);
+        if (other) {
+          before += __builtin_ctzll(other);
+          break;
+        }
+        before += 64;
+      }
+      if (before & 1) return;  // (the block in front takes this one along)
+      blocks = next == e ? 2 : 1;
+    }
+    if ((int64_t)b * a.block_m >= *a.ntpp || e < 0 || e >= a.E) return;
   }
-  const int slot = (lane & 15) < a.block_m ? slot_at(a, (int64_t)b * a.block_m + (lane & 15)) : -1;
-  if (__ballot(slot >= 0) == 0) return;  // (the same in every wave)
-
   const int KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   const int kt0 = KT * w / KS, kt1 = KT * (w + 1) / KS;
   const int koff = 16 * (lane >> 4);
-  const int64_t row = slot >= 0 ? slot / a.top_k : 0;
-  const uint8_t* xp = a.A + row * a.lda + koff;
+  int slot[MB];
+  const uint8_t* xp[MB];
+  const float* sap[MB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m) {
+    slot[m] = (lane & 15) < a.block_m && m < blocks ? slot_at(a, (int64_t)(b + m) * a.block_m + (lane & 15)) : -1;
+    const int64_t row = slot[m] >= 0 ? slot[m] / a.top_k : 0;
+    xp[m] = a.A + row * a.lda + koff;
+    if constexpr (T::kScaled) sap[m] = a.sa + row * a.ld_sa;
+  }
   const uint8_t* wp[NG];
   const float* sbp[NG];
-  const float* sap = nullptr;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int n = min((strip * NG + g) * 16 + (lane & 15), a.N - 1);
@@ -135,64 +154,86 @@ __global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArg
     if constexpr (T::kScaled)
       sbp[g] = a.sb + ((int64_t)e * ((a.N + kScaleBlock - 1) / kScaleBlock) + n / kScaleBlock) * KT;
   }
-  if constexpr (T::kScaled) sap = a.sa + row * a.ld_sa;
   const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
 
-  f32x4_t acc[NG];
+  f32x4_t acc[NG][MB];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[g][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int c = kt0; c < kt1; c += kChunk) {
-    Frag x[kChunk], wt[kChunk][NG];
-    float sa[kChunk], sb[kChunk][NG];
+    Frag x[kChunk][MB], wt[kChunk][NG];
+    float sa[kChunk][MB], sb[kChunk][NG];
 #pragma unroll
     for (int u = 0; u < kChunk; ++u) {
       const int kt = min(c + u, kt1 - 1);  // (past the wave's last step: loaded again, not used)
       const int64_t k0 = (int64_t)kt * kStepBytes;
-      const bool lo = k0 + koff < a.Kb && slot >= 0, hi = k0 + koff + 64 < a.Kb && slot >= 0;
-      const bool wlo = k0 + koff < a.Kb, whi = k0 + koff + 64 < a.Kb;
-      x[u] = load_frag(lo ? xp + k0 : zero, hi ? xp + k0 + 64 : zero);
+      const bool lo = k0 + koff < a.Kb, hi = k0 + koff + 64 < a.Kb;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        wt[u][g] = load_frag(wlo ? wp[g] + k0 : zero, whi ? wp[g] + k0 + 64 : zero);
+        wt[u][g] = load_frag(lo ? wp[g] + k0 : zero, hi ? wp[g] + k0 + 64 : zero);
         if constexpr (T::kScaled) sb[u][g] = sbp[g][kt];
       }
-      if constexpr (T::kScaled) sa[u] = sap[kt];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        x[u][m] = load_frag(lo && slot[m] >= 0 ? xp[m] + k0 : zero, hi && slot[m] >= 0 ? xp[m] + k0 + 64 : zero);
+        if constexpr (T::kScaled) sa[u][m] = sap[m][kt];
+      }
     }
+    // (eight waves: all of a chunk's loads in flight; with more workgroups a CU the compiler's order, which
+    // keeps fewer registers and more of them resident, is the faster one)
+    if constexpr (KS == 8) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < kChunk; ++u) {
       if (c + u >= kt1) break;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if constexpr (T::kScaled) {
-          const f32x4_t t = mfma_step(T{}, wt[u][g], x[u]);
-          // (the scale of the weight block belongs to the tile's rows: lane l's row of the operand
-          // and the rows of its result lie in one 16-row tile, hence in one block)
-          const float s = sa[u] * sb[u][g];
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[g][q] = fmaf(t[q], s, acc[g][q]);
-        } else {
-          acc[g] = mfma_step(T{}, wt[u][g], x[u], acc[g]);
+        for (int m = 0; m < MB; ++m) {
+          if constexpr (T::kScaled) {
+            const f32x4_t t = mfma_step(T{}, wt[u][g], x[u][m]);
+            // (the scale of the weight block belongs to the tile's rows: lane l's row of the operand
+            // and the rows of its result lie in one 16-row tile, hence in one block)
+            const float s = sa[u][m] * sb[u][g];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[g][m][q] = fmaf(t[q], s, acc[g][m][q]);
+          } else {
+            acc[g][m] = mfma_step(T{}, wt[u][g], x[u][m], acc[g][m]);
+          }
         }
-      }
     }
   }
 #pragma unroll
-  for (int g = 0; g < NG; ++g) part[w][g][lane] = acc[g];
-  __syncthreads();
-  for (int g = w; g < NG; g += KS) {
-    f32x4_t v = part[0][g][lane];
+  for (int g = 0; g < NG; ++g)
 #pragma unroll
-    for (int i = 1; i < KS; ++i) v += part[i][g][lane];
+    for (int m = 0; m < MB; ++m) part[w][g * MB + m][lane] = acc[g][m];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NG * MB; ++i) {
+    if (i % KS != w) continue;
+    const int g = i / MB, m = i % MB;
+    f32x4_t v = part[0][i][lane];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) v += part[k][i][lane];
     const int n0 = (strip * NG + g) * 16 + 4 * (lane >> 4);
-    if (n0 < a.N && slot >= 0) {  // (N is a multiple of 8: four columns are in or out together)
+    if (n0 < a.N && slot[m] >= 0) {  // (N is a multiple of 8: four columns are in or out together)
       if (a.bias) {
         const u32x2_t bb = *reinterpret_cast<const u32x2_t*>(a.bias + (int64_t)e * a.N + n0);
         v[0] += bf16_lo(bb[0]); v[1] += bf16_hi(bb[0]); v[2] += bf16_lo(bb[1]); v[3] += bf16_hi(bb[1]);
       }
-      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.C) + (int64_t)slot * a.ldc + n0) =
+      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.C) + (int64_t)slot[m] * a.ldc + n0) =
           u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
   }
+}
+
+template <typename T, int NG, int KS, int MB>
+static int launch_stream(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipStream_t st) {
+  a.cap_blocks = (int32_t)cap_blocks;
+  const int64_t grid = (int64_t)((a.N + 16 * NG - 1) / (16 * NG)) * cap_blocks;
+  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+  hipLaunchKernelGGL((block_gemm_stream_kernel<T, NG, KS, MB>), dim3((unsigned)grid), dim3(64 * KS), 0, st, a);
+  return check_launch(fn);
 }
 
 // ---------------------------------------------------------------------------- blocks of rows
@@ -681,46 +722,61 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
 }
 
 // The kernel for a call.  Blocks of at most 16 rows stream their weights (block_gemm_stream_kernel).  For
-// the others the tile with the least rounds x time of a step (one step of 128 bytes of K of all the
-// workgroups that are resident, measured for e4m3fn; bf16's have the same proportions):
-//   256 x 256, one workgroup a CU: 1.87 us     128 x 256, one a CU: 1.08 us
-//   128 x 128, two a CU: 1.17 us                64 x 64, two a CU: 0.45 us
-// Blocks of at most 64 rows have no use for the larger ones: 64 x 256 or 32 x 256, and 64 x 64 where
-// these leave CUs without work.  256-row tiles are made of an expert's 128-row blocks, counted in the
-// kernel, where the batch has 512 slots an expert (fewer leave its last, partly filled tile too large a
-// share: 1024 tokens of 8 choices on 32 local experts 614 us with 128 rows, 655 with 256).
+// the others the tile shape with the least rounds of resident workgroups (half way between the whole
+// number and the fraction: later ones start as earlier ones end) x time of one, for KT steps of 128 bytes of K (fitted to dense e4m3fn products of 8 to 56 steps; bf16's have the same proportions):
+//   256 x 256, one a CU    10.4 + 1.68 KT us        128 x 128, two a CU   5.7 + 1.18 KT us
+//   128 x 256, one a CU     6.4 + 1.07 KT us         64 x 64, two a CU    2.8 + 0.51 KT us
+//    64 x 256, one a CU     3.6 + 0.70 KT us
+// and 4 us more for finding the tile's expert and rows.  The rows of routed experts are taken as spread
+// evenly, each expert ending half way through a tile.  256-row tiles are made of an expert's 128-row blocks, counted in the kernel (7 us more), where the
+// batch has 512 slots an expert: with fewer the last, partly filled tile is too large a share (1024
+// Zipf tokens of 8 choices on 32 of 256 experts: 614 us with 128 rows, 655 us with 256).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
-  if constexpr (!T::kTrans) if (a.block_m <= 16) {
-    constexpr int NG = 2, KS = 4;
-    const int64_t grid = (int64_t)((a.N + 16 * NG - 1) / (16 * NG)) * cap_blocks;
-    MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-    hipLaunchKernelGGL((block_gemm_stream_kernel<T, NG, KS>), dim3((unsigned)grid), dim3(64 * KS), 0, st, a);
-    return check_launch(fn);
+  if constexpr (!T::kTrans) {
+    if (a.block_m <= 16) {
+      // Two tiles and four waves a workgroup, or one tile where that leaves CUs with one workgroup or none,
+      // with eight waves along a long K (a dense row, N = 4096: K = 7168 15.6, 12.1, 8.4 us for the three;
+      // K = 512 3.8, 3.4, 5.0 us).  Four tiles and two blocks of an expert together where experts have more
+      // rows than one block holds often enough (16 slots each on 128 experts, N = K = 2880: 302 -> 245 us;
+      // with 2 slots each on 32 experts nothing is gained, 139 and 140 us).
+      const int64_t cus = device_cu_count(), n = (int64_t)((a.N + 31) / 32) * cap_blocks;
+      if (n < cus && a.Kb >= 24 * kStepBytes) return launch_stream<T, 1, 8, 1>(fn, a, cap_blocks, st);
+      if (n < 2 * cus) return launch_stream<T, 1, 4, 1>(fn, a, cap_blocks, st);
+      if (a.sorted && a.numel >= 10ll * a.E) return launch_stream<T, 4, 4, 2>(fn, a, cap_blocks, st);
+      return launch_stream<T, 2, 4, 1>(fn, a, cap_blocks, st);
+    }
   }
-  const int64_t cus = device_cu_count();
-  auto count = [&](int BM, int BN) { return cap_blocks * ((a.block_m + BM - 1) / BM) * ((a.N + BN - 1) / BN); };
-  if (a.block_m <= 32) {
-    if (count(32, 256) < cus) return launch_tile<T, 2, 1, 1, 4, 4>(fn, a, cap_blocks, st);
-    return launch_tile<T, 2, 4, 1, 4, 2>(fn, a, cap_blocks, st);
-  }
-  if (a.block_m <= 64) {
-    if (count(64, 256) < cus) return launch_tile<T, 2, 2, 2, 2, 4>(fn, a, cap_blocks, st);
-    return launch_tile<T, 2, 4, 2, 4, 3>(fn, a, cap_blocks, st);
-  }
+  const int64_t cus = device_cu_count(), KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   constexpr int64_t kMaxMerged = 16384;  // blocks whose experts fit the kernel's LDS
   const bool merge = a.sorted && a.block_m == 128 && cap_blocks <= kMaxMerged && a.numel >= 512ll * a.E;
-  auto rounds = [&](int64_t n, int per_cu) { return (double)((n + cus * per_cu - 1) / (cus * per_cu)); };
-  const double big = merge ? rounds((count(128, 256) + 1) / 2, 1) * 1.87
-                           : (a.sorted && a.block_m <= 128 ? 1e30 : rounds(count(256, 256), 1) * 1.87);
-  const double mid = rounds(count(128, 256), 1) * 1.08, low = rounds(count(128, 128), 2) * 1.17;
-  const double small = rounds(count(64, 64), 2) * 0.45;
-  if (big <= std::min({mid, low, small})) {
+  auto cost = [&](int BM, int BN, int per_cu, double fixed, double step) {
+    const int64_t tiles = a.sorted ? std::min(cap_blocks * ((a.block_m + BM - 1) / BM),
+                                              a.numel / BM + (std::min<int64_t>(a.E, a.numel) + 1) / 2)
+                                   : ((int64_t)a.numel + BM - 1) / BM;
+    const int64_t n = tiles * ((a.N + BN - 1) / BN);
+    const double exact = std::max(1.0, (double)n / (double)(cus * per_cu));
+    const double whole = (double)((n + cus * per_cu - 1) / (cus * per_cu));
+    return (exact + whole) / 2 * (fixed + (a.sorted ? 4.0 : 0.0) + step * (double)KT);
+  };
+  const double small = cost(64, 64, 2, 2.8, 0.51), flat = cost(64, 256, 1, 3.6, 0.70);
+  if (a.block_m <= 32) {  // (at most 32 rows: the 64-row tiles' shapes with half the rows)
+    if (small < flat) return launch_tile<T, 2, 1, 1, 4, 4>(fn, a, cap_blocks, st);
+    return launch_tile<T, 2, 4, 1, 4, 2>(fn, a, cap_blocks, st);
+  }
+  const double never = 1e30;
+  const bool rows128 = a.block_m > 64, rows256 = merge || !a.sorted || a.block_m == 256;
+  const double low = rows128 ? cost(128, 128, 2, 5.7, 1.18) : never;
+  const double mid = rows128 ? cost(128, 256, 1, 6.4, 1.07) : never;
+  const double big = rows256 ? cost(256, 256, 1, merge ? 17.4 : 10.4, 1.68) : never;
+  const double best = std::min({small, flat, low, mid, big});
+  if (big == best) {
     if (merge) return launch_tile<T, 8, 4, 2, 4, 2, true>(fn, a, cap_blocks, st);
     return launch_tile<T, 8, 4, 2, 4, 2>(fn, a, cap_blocks, st);
   }
-  if (mid <= std::min(low, small)) return launch_tile<T, 4, 4, 2, 4, 3>(fn, a, cap_blocks, st);
-  if (low <= small) return launch_tile<T, 4, 4, 2, 2, 2>(fn, a, cap_blocks, st);
+  if (mid == best) return launch_tile<T, 4, 4, 2, 4, 3>(fn, a, cap_blocks, st);
+  if (low == best) return launch_tile<T, 4, 4, 2, 2, 2>(fn, a, cap_blocks, st);
+  if (flat == best) return launch_tile<T, 2, 4, 2, 4, 3>(fn, a, cap_blocks, st);
   return launch_tile<T, 2, 2, 2, 2, 4>(fn, a, cap_blocks, st);
 }
 
