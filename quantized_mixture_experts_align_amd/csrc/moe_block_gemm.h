@@ -363,53 +363,35 @@ __host__ __device__ inline void unit_tile(int P, int strips, int group_m, int gr
   strip = u % across * group_n + r / group_m;
 }
 
-// The workgroup's tile when tiles of BM entries are made of several blocks: an expert's blocks follow
-// each other, and the ones whose number within the expert is a multiple of BM / block_m start a tile.
-// Tile t's first block and its entries (0 behind the last tile).  Every thread calls it; `lds` holds an
-// int for each block of the capacity.  (The tiles are counted here, by each workgroup for itself, so
-// that no launch has to come before and the live tiles lie side by side for the XCDs.)
-__device__ __forceinline__ int merged_tile(const BlockGemmArgs& a, int cap_blocks, int BM, int t, int* lds, int* block) {
+// A tile of BM entries made of several blocks: an expert's blocks follow each other, and the ones whose
+// number within the expert is a multiple of BM / block_m start a tile.  Gives tile t's first block, its
+// expert and its entries (0 behind the last tile), each wave for itself with 64 blocks at a time.  (The
+// tiles are counted here, by each workgroup for itself, so that no launch has to come before and the
+// live tiles lie side by side for the XCDs.)
+__device__ __forceinline__ int merged_tile(const BlockGemmArgs& a, int nb, int BM, int t, int* block, int* expert) {
   const int lane = threadIdx.x & 63, per = BM / a.block_m;
-  for (int i = threadIdx.x; i < cap_blocks; i += blockDim.x) lds[i] = a.eids[i];
-  __syncthreads();
-  const int c = (cap_blocks + 63) / 64, i0 = min(lane * c, cap_blocks), i1 = min(i0 + c, cap_blocks);
-  auto at = [&](int i) { return i >= 0 && i < cap_blocks ? lds[i] : -1; };
-  auto live = [&](int e) { return e >= 0 && e < a.E; };
-  int begin = -1;  // the last block of the lane's share that begins an expert
-  for (int i = i0; i < i1; ++i)
-    if (at(i) != at(i - 1)) begin = i;
-  int before = __shfl_up(begin, 1);
-  if (lane == 0) before = 0;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(before, d);
-    if (lane >= d) before = max(before, o);
-  }
-  int tiles = 0, from = max(before, 0);
-  for (int i = i0; i < i1; ++i) {
-    if (at(i) != at(i - 1)) from = i;
-    tiles += live(at(i)) && (i - from) % per == 0;
-  }
-  int sum = tiles;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
-  int found = -1, left = t - (sum - tiles);
-  if (left >= 0 && left < tiles) {
-    from = max(before, 0);
-    for (int i = i0; i < i1 && found < 0; ++i) {
-      if (at(i) != at(i - 1)) from = i;
-      if (live(at(i)) && (i - from) % per == 0 && left-- == 0) found = i;
+  int from = 0;  // where the current expert's blocks begin
+  for (int base = 0; base < nb; base += 64) {
+    const int i = base + lane;
+    const int e = i < nb ? a.eids[i] : -1, prev = i > 0 && i <= nb ? a.eids[i - 1] : -2;
+    const uint64_t begins = __ballot(e != prev);
+    const uint64_t upto = begins & (~0ull >> (63 - lane));
+    const int mine = upto ? base + 63 - __clzll((long long)upto) : from;
+    uint64_t starts = __ballot(e >= 0 && e < a.E && (i - mine) % per == 0);
+    const int n = __popcll(starts);
+    if (t < n) {
+      for (; t > 0; --t) starts &= starts - 1;
+      const int l = __builtin_ctzll(starts);
+      *block = base + l;
+      *expert = __builtin_amdgcn_readlane(e, l);
+      int blocks = 1;
+      while (blocks < per && base + l + blocks < nb && a.eids[base + l + blocks] == *expert) ++blocks;
+      return blocks * a.block_m;
     }
+    t -= n;
+    if (begins) from = base + 63 - __clzll((long long)begins);
   }
-  const uint64_t who = __ballot(found >= 0);
-  if (!who) return 0;
-  found = __shfl(found, __builtin_ctzll(who));
-  const int e = at(found);
-  int n = 1;
-  while (n < per && at(found + n) == e) ++n;
-  *block = __builtin_amdgcn_readfirstlane(found);
-  return __builtin_amdgcn_readfirstlane(n) * a.block_m;
+  return 0;
 }
 
 // Workgroup = WM x WN waves over BM = 16 * MG * WM rows of one block x BN = 16 * NG * WN weight rows;
@@ -451,9 +433,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
   const int sub = kMerge ? 0 : mb - b * subs;
   int rows = min(a.block_m - sub * BM, BM);
   if constexpr (kMerge) {
-    rows = merged_tile(a, a.cap_blocks, BM, mb, reinterpret_cast<int*>(smem), &b);
+    const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), per = BM / a.block_m;
+    if (mb * per >= nb + min(a.E, nb) * (per - 1)) return;  // (more tiles than these blocks can make)
+    rows = merged_tile(a, nb, BM, mb, &b, &e);
     if (rows == 0) return;
-    __syncthreads();  // (the blocks' experts have been read: the first loads may take their place)
   }
   // A workgroup is alone on its CU, so its start is not hidden: everything that says what it works on
   // is asked for at once (entries behind the live blocks exist, so no load waits for the block count)
@@ -466,7 +449,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
     xs[l] = r < rows ? slot_at(a, first + r) : -1;
   }
   if (T::kScaled && lane % SR + w * SR < rows) ss = slot_at(a, first + w * SR + lane % SR);
-  if (a.sorted) {
+  if (!kMerge && a.sorted) {
     const int nb = *a.ntpp / a.block_m;
     e = a.eids[b];
     if (b >= nb || e < 0 || e >= a.E) return;
@@ -748,7 +731,7 @@ static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap
     }
   }
   const int64_t cus = device_cu_count(), KT = (a.Kb + kStepBytes - 1) / kStepBytes;
-  constexpr int64_t kMaxMerged = 16384;  // blocks whose experts fit the kernel's LDS
+  constexpr int64_t kMaxMerged = 4096;  // blocks that every workgroup counts through, 64 at a time
   const bool merge = a.sorted && a.block_m == 128 && cap_blocks <= kMaxMerged && a.numel >= 512ll * a.E;
   auto cost = [&](int BM, int BN, int per_cu, double fixed, double step) {
     const int64_t tiles = a.sorted ? std::min(cap_blocks * ((a.block_m + BM - 1) / BM),
