@@ -154,6 +154,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
   for (int g = 0; g < NG; ++g)
 #pragma unroll
     for (int h = 0; h < MG; ++h) acc[g][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // dbias is the same reduction with ones in the place of A: the waves of the first tile of columns that
+  // own its first 16 (wn = 0) take it along, two products more for each of the 2 NG.
+  const bool ones = a.dbias && kt0 == 0 && wn == 0;
+  f32x4_t accb[MG];
+#pragma unroll
+  for (int h = 0; h < MG; ++h) accb[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const u32x4_t one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   if (KT > 0) {
     int coff[MG], xoff[NG];
 #pragma unroll
@@ -205,6 +212,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
             acc[g][h] = mfma(xf[sub][g], cf[sub], acc[g][h]);
             if (h + 1 == MG) xf[sub][g] = read_x(next, sub, g);
           }
+        if (ones) {
+          accb[h] = mfma(one, cf[0], accb[h]);
+          accb[h] = mfma(one, cf[1], accb[h]);
+        }
         __builtin_amdgcn_sched_barrier(0);
         cf[0] = cn[0];
         cf[1] = cn[1];
@@ -214,51 +225,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
     wait_vm<0>();
     block_barrier();
   }
+  if (ones && lane < 16) {  // (every row of the product is the sum; lane l < 16 holds row 0 of column l)
+#pragma unroll
+    for (int h = 0; h < MG; ++h) {
+      const int n = n0 + (wm * MG + h) * 16 + lane;
+      if (n >= a.N) continue;
+      const int64_t at = (int64_t)e * a.N + n;
+      if constexpr (sizeof(OUT) == 4) static_cast<float*>(a.dbias)[at] = accb[h][0];
+      else static_cast<uint16_t*>(a.dbias)[at] = f32_to_bf16(accb[h][0]);
+    }
+  }
   store_tiles<NG, MG, OUT>(acc, MG, smem, w, lane, k0 + wn * 16 * NG, a.K, true, [&](int r) -> OUT* {
     const int n = n0 + wm * 16 * MG + r;
     return n < a.N ? static_cast<OUT*>(a.dW) + ((int64_t)e * a.N + n) * a.K : nullptr;
   });
-}
-
-// dbias[e, n] of 128 columns: 16 chunks of eight columns x 16 rows at a time, joined in row order.
-template <typename OUT>
-__global__ __launch_bounds__(256) void bias_grad_kernel(GradArgs a) {
-  __shared__ int red[8];
-  __shared__ float part[16][128];
-  const int tid = threadIdx.x, r = tid >> 4, c8 = (tid & 15) * 8;
-  const int ns = (a.N + 127) / 128, nt = blockIdx.x % ns, e = blockIdx.x / ns;
-  int64_t first, last;
-  expert_range(a, e, red, &first, &last);
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  const int n = nt * 128 + c8;
-  for (int64_t p = first + r; p < last; p += 16 * 8) {  // eight rows in flight a thread
-    u32x4_t c[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int s = p + 16 * u < last ? a.sorted[p + 16 * u] : -1;
-      c[u] = u32x4_t{0u, 0u, 0u, 0u};
-      if (s >= 0 && s < a.numel && n < a.N) c[u] = *reinterpret_cast<const u32x4_t*>(a.dC + (int64_t)s * a.ld_dc + n);
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] += bf16_lo(c[u][j]);
-        v[2 * j + 1] += bf16_hi(c[u][j]);
-      }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) part[r][c8 + j] = v[j];
-  __syncthreads();
-  if (tid < 128 && nt * 128 + tid < a.N) {
-    float t = 0.f;
-    for (int i = 0; i < 16; ++i) t += part[i][tid];
-    const int64_t at = (int64_t)e * a.N + nt * 128 + tid;
-    if constexpr (sizeof(OUT) == 4) static_cast<float*>(a.dbias)[at] = t;
-    else static_cast<uint16_t*>(a.dbias)[at] = f32_to_bf16(t);
-  }
 }
 
 // dst[r, :] = sum over the live slots of row r, in slot order (fp32, one rounding), of src[slot, :]
@@ -407,10 +387,5 @@ extern "C" int moe_bf16_gemm_wgrad(const uint16_t* dC, int64_t ld_dc, const uint
     while ((2u << a.div_shift) < (uint32_t)top_k) ++a.div_shift;
     a.div_mul = (uint32_t)(((1ull << (32 + a.div_shift)) + top_k - 1) / (uint64_t)top_k);
   }
-  rc = out_f32 ? launch_wgrad<float>(fn, a, stream) : launch_wgrad<uint16_t>(fn, a, stream);
-  if (rc || !dbias) return rc;
-  const unsigned gb = (unsigned)((int64_t)((N + 127) / 128) * E);
-  if (out_f32) hipLaunchKernelGGL(bias_grad_kernel<float>, dim3(gb), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL(bias_grad_kernel<uint16_t>, dim3(gb), dim3(256), 0, stream, a);
-  return check_launch(fn);
+  return out_f32 ? launch_wgrad<float>(fn, a, stream) : launch_wgrad<uint16_t>(fn, a, stream);
 }

@@ -11,19 +11,24 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from .ops import align_capacity
-
 GROUP = 128           # columns that share an activation scale, rows and columns of a weight block
 _F8 = (torch.float8_e4m3fn, torch.uint8)
 
 
+_entry = {}           # C entry points, looked up once
+_raw_stream = torch._C._cuda_getCurrentRawStream   # (a stream's handle without a Stream object: 0.1 us, not 2.6)
+
+
 def _call(dev: torch.device, name: str, *args) -> None:
-    f = getattr(L.lib(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = f(*args, torch.cuda.current_stream().cuda_stream)
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(L.lib(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch.cuda.current_stream().cuda_stream)
+            rc = f(*args, _raw_stream(index))
     if rc:
         L.check(rc, name)
 
@@ -55,11 +60,19 @@ def _ld(t: torch.Tensor) -> int:
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 
 
+def _capacity(numel: int, E: int, block_m: int):
+    """moe_align_capacity's slots and blocks (the entry points check the arguments themselves)."""
+    if block_m < 1 or numel < 0:
+        raise ValueError(f"numel={numel} block_m={block_m}")
+    blocks = -(-(numel + min(E, numel) * (block_m - 1)) // block_m)
+    return blocks * block_m, blocks
+
+
 def _check_align(sorted_token_ids, expert_ids, num_tokens_post_padded, numel: int, E: int, block_m: int, dev) -> None:
     for t, name in ((sorted_token_ids, "sorted_token_ids"), (expert_ids, "expert_ids"),
                     (num_tokens_post_padded, "num_tokens_post_padded")):
         _check(t, name, _I32, dev=dev)
-    s_len, b_len = align_capacity(numel, 1, E, block_m)
+    s_len, b_len = _capacity(numel, E, block_m)
     if sorted_token_ids.numel() < s_len or expert_ids.numel() < b_len or num_tokens_post_padded.numel() < 1:
         raise ValueError(f"the align's outputs hold {sorted_token_ids.numel()} slots and {expert_ids.numel()} blocks; "
                          f"{numel} slots on {E} experts in blocks of {block_m} need {s_len} and {b_len}")
@@ -184,10 +197,29 @@ def moe_bf16_gemm(A: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tens
         out = torch.empty((numel, N), dtype=torch.bfloat16, device=dev)
     else:
         _check(out, "out", _BF16, (numel, N), dev, rows=True)
-    _call(dev, "moe_bf16_gemm", A.data_ptr(), A.shape[0], _ld(A), W.data_ptr(),
-          None if bias is None else bias.data_ptr(), E, N, K, out.data_ptr(), _ld(out), sorted_token_ids.data_ptr(),
-          expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), numel, top_k, block_m)
+    _bf16_gemm(A, W, sorted_token_ids, expert_ids, num_tokens_post_padded, numel, top_k, block_m, bias, out)
     return out
+
+
+# (the calls proper, for tensors that have been checked)
+def _bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, numel, top_k, block_m, bias, out) -> None:
+    E, N, K = W.shape
+    _call(A.device, "moe_bf16_gemm", A.data_ptr(), A.shape[0], _ld(A), W.data_ptr(),
+          None if bias is None else bias.data_ptr(), E, N, K, out.data_ptr(), _ld(out), sorted_ids.data_ptr(),
+          expert_ids.data_ptr(), ntpp.data_ptr(), numel, top_k, block_m)
+
+
+def _dgrad(dC, W, sorted_ids, expert_ids, ntpp, live: int, top_k, block_m, out, work) -> None:
+    E, N, K = W.shape
+    _call(dC.device, "moe_bf16_gemm_dgrad", dC.data_ptr(), _ld(dC), W.data_ptr(), E, N, K, out.data_ptr(), _ld(out),
+          sorted_ids.data_ptr(), expert_ids.data_ptr(), ntpp.data_ptr(), live, dC.shape[0], top_k, block_m,
+          None if work is None else work.data_ptr(), 0 if work is None else work.numel())
+
+
+def _wgrad(dC, A, E, sorted_ids, expert_ids, ntpp, top_k, block_m, out, out_bias) -> None:
+    _call(dC.device, "moe_bf16_gemm_wgrad", dC.data_ptr(), _ld(dC), A.data_ptr(), A.shape[0], _ld(A), E, dC.shape[1],
+          A.shape[1], out.data_ptr(), None if out_bias is None else out_bias.data_ptr(), int(out.dtype is torch.float32),
+          sorted_ids.data_ptr(), expert_ids.data_ptr(), ntpp.data_ptr(), dC.shape[0], top_k, block_m)
 
 
 def moe_bf16_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tensor, expert_ids: torch.Tensor,
@@ -219,9 +251,7 @@ def moe_bf16_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, sorted_token_ids: tor
             _check(work, "work", _F32, dev=dev)
     else:
         work = None
-    _call(dev, "moe_bf16_gemm_dgrad", dC.data_ptr(), _ld(dC), W.data_ptr(), E, N, K, out.data_ptr(), _ld(out),
-          sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), live, numel, top_k,
-          block_m, None if work is None else work.data_ptr(), 0 if work is None else work.numel())
+    _dgrad(dC, W, sorted_token_ids, expert_ids, num_tokens_post_padded, live, top_k, block_m, out, work)
     return out
 
 
@@ -250,9 +280,7 @@ def moe_bf16_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, n_experts: int, sorte
             _check(out_bias, "out_bias", (dtype,), (E, N), dev)
     else:
         out_bias = None
-    _call(dev, "moe_bf16_gemm_wgrad", dC.data_ptr(), _ld(dC), A.data_ptr(), A.shape[0], _ld(A), E, N, K, out.data_ptr(),
-          None if out_bias is None else out_bias.data_ptr(), int(dtype is torch.float32), sorted_token_ids.data_ptr(),
-          expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), numel, top_k, block_m)
+    _wgrad(dC, A, E, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, out, out_bias)
     return out, out_bias
 
 
@@ -277,16 +305,20 @@ class _ExpertsLinear(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        A, W, sorted_ids, expert_ids, ntpp, slot_local = ctx.saved_tensors
+        A, W, *align, slot_local = ctx.saved_tensors
         # (a gradient may arrive broadcast or transposed, or with rows too close for 16-byte loads)
         if grad.stride(-1) != 1 or grad.stride(0) % 8 or grad.stride(0) < grad.shape[1] or grad.data_ptr() % 16:
             grad = grad.contiguous()
         dA = dW = db = None
         if ctx.needs_input_grad[0]:
-            dA = moe_bf16_gemm_dgrad(grad, W, sorted_ids, expert_ids, ntpp, slot_local, ctx.top_k, ctx.block_m)
+            dA = torch.empty(A.shape, dtype=A.dtype, device=A.device)
+            work = None if ctx.top_k == 1 else torch.empty(grad.shape[0] * W.shape[2], dtype=torch.float32, device=A.device)
+            _dgrad(grad, W, *align, slot_local.data_ptr(), ctx.top_k, ctx.block_m, dA, work)
         if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
-            dW, db = moe_bf16_gemm_wgrad(grad, A, W.shape[0], sorted_ids, expert_ids, ntpp, ctx.top_k, ctx.block_m,
-                                         bias_grad=ctx.has_bias and ctx.needs_input_grad[2])
+            dW = torch.empty_like(W)
+            if ctx.has_bias and ctx.needs_input_grad[2]:
+                db = torch.empty(W.shape[:2], dtype=W.dtype, device=W.device)
+            _wgrad(grad, A, W.shape[0], *align, ctx.top_k, ctx.block_m, dW, db)
         return dA, dW, db, None, None, None, None, None, None
 
 
