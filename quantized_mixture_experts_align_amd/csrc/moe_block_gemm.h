@@ -407,41 +407,41 @@ __device__ __forceinline__ int merged_tile(const BlockGemmArgs& a, int nb, int B
 // Step kt + kStages - 1 is requested when step kt starts.  The step's closing wait and barrier come
 // before the products of its last row group, whose operands are in registers by then: the first
 // operands of the next step are read from LDS behind those products.
-template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge>
-// (two waves a SIMD: one workgroup of eight waves a CU, or two of four)
-__global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockGemmArgs a) {
-  constexpr int WAVES = WM * WN, BM = 16 * MG * WM, BN = 16 * NG * WN;
-  constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;   // direct loads per wave and step, eight rows each
+template <typename T, int MG, int NG, int WM, int WN, int kStages>
+struct TileShape {
+  static constexpr int WAVES = WM * WN, BM = 16 * MG * WM, BN = 16 * NG * WN;
+  static constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;   // direct loads per wave and step, 1 KB each
   static_assert(XI * 8 * WAVES == BM && WI * 8 * WAVES == BN, "the waves share the staged rows evenly");
-  constexpr int SR = BM / WAVES, SP = SR + 4;               // rows whose scales a wave loads; its place for them
-  constexpr int XB = BM * kStepBytes, WB = BN * kStepBytes;
-  constexpr int STAGE = XB + WB + (T::kScaled ? WAVES * SP * 4 : 0);
+  static constexpr int SR = BM / WAVES, SP = SR + 4;  // rows whose scales a wave loads; its place for them
+  static constexpr int XB = BM * kStepBytes, WB = BN * kStepBytes;
+  static constexpr int STAGE = XB + WB + (T::kScaled ? WAVES * SP * 4 : 0);
+  static constexpr int BYTES = kStages * STAGE;
+  static_assert(BYTES >= WAVES * 16 * (32 * NG + 16), "the epilogue's staging fits");
+};
+
+template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge>
+constexpr int tile_bytes() {
+  constexpr int full = TileShape<T, MG, NG, WM, WN, kStages>::BYTES;
+  if constexpr (kMerge) {
+    constexpr int half = TileShape<T, MG / 2, NG, WM, WN, kStages + 1>::BYTES;
+    return half > full ? half : full;
+  }
+  return full;
+}
+
+// One tile: the `rows` sorted entries from `first` on, of expert e, and strip `strip` of its weights.
+template <typename T, int MG, int NG, int WM, int WN, int kStages>
+__device__ __forceinline__ void gemm_tile(const BlockGemmArgs& a, uint8_t* smem, int* s_slot, int64_t first, int rows,
+                                          int e, int strip) {
+  typedef TileShape<T, MG, NG, WM, WN, kStages> Shape;
+  constexpr int BM = Shape::BM, BN = Shape::BN, XI = Shape::XI, WI = Shape::WI, SR = Shape::SR, SP = Shape::SP;
+  constexpr int XB = Shape::XB, WB = Shape::WB, STAGE = Shape::STAGE;
   constexpr int LOADS = XI + WI + (T::kScaled ? 1 : 0);
   constexpr int SPREAD = kStages > 2 && MG > 2 ? MG - 1 : (MG > 2 ? 2 : 1);  // row groups over which the loads are spread
-  static_assert(kStages * STAGE >= WAVES * 16 * (32 * NG + 16), "the epilogue's staging fits");
-  __shared__ __attribute__((aligned(128))) uint8_t smem[kStages * STAGE];
-  __shared__ int s_slot[BM];
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = w / WN, wn = w % WN;
 
-  const int strips = (a.N + BN - 1) / BN, subs = (a.block_m + BM - 1) / BM;
-  int mb, strip;
-  unit_tile(blockIdx.x, strips, a.group_m, a.group_n, mb, strip);
-  if (mb >= a.tiles || strip >= strips) return;
-  int b = mb / subs, e = 0;
-  const int sub = kMerge ? 0 : mb - b * subs;
-  int rows = min(a.block_m - sub * BM, BM);
-  if constexpr (kMerge) {
-    const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), per = BM / a.block_m;
-    if (mb * per >= nb + min(a.E, nb) * (per - 1)) return;  // (more tiles than these blocks can make)
-    rows = merged_tile(a, nb, BM, mb, &b, &e);
-    if (rows == 0) return;
-  }
-  // A workgroup is alone on its CU, so its start is not hidden: everything that says what it works on
-  // is asked for at once (entries behind the live blocks exist, so no load waits for the block count)
-  // and the first steps' operands before the tile's rows are counted.
-  const int64_t first = (int64_t)b * a.block_m + sub * BM;
   int xs[XI], ss = -1;
 #pragma unroll
   for (int l = 0; l < XI; ++l) {
@@ -449,12 +449,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
     xs[l] = r < rows ? slot_at(a, first + r) : -1;
   }
   if (T::kScaled && lane % SR + w * SR < rows) ss = slot_at(a, first + w * SR + lane % SR);
-  if (!kMerge && a.sorted) {
-    const int nb = *a.ntpp / a.block_m;
-    e = a.eids[b];
-    if (b >= nb || e < 0 || e >= a.E) return;
-  }
-
   const int KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   const bool ragged = a.Kb % kStepBytes != 0;
   const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
@@ -678,6 +672,45 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
     const int s = s_slot[((r >> 4) * WM + wm) * 16 + (r & 15)];
     return s >= 0 ? static_cast<Out*>(a.C) + (int64_t)s * a.ldc : nullptr;
   });
+}
+
+// A workgroup is alone on its CU (or one of two), so its start is not hidden: what says which rows it works
+// on is asked for at once (entries behind the live blocks exist, so no load waits for the block count),
+// and the first steps' operands before the tile's rows are counted.  (two waves a SIMD: one workgroup of
+// eight waves a CU, or two of four.)
+//
+// With kMerge a tile of BM rows is made of several blocks of an expert, and an expert's last tile that
+// holds no more than half of them runs in the shape of half the rows with a stage more: a step of a half
+// filled tile costs nearly what a full one's does.
+template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge>
+__global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockGemmArgs a) {
+  constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
+  __shared__ __attribute__((aligned(128))) uint8_t smem[tile_bytes<T, MG, NG, WM, WN, kStages, kMerge>()];
+  __shared__ int s_slot[BM];
+  const int strips = (a.N + BN - 1) / BN, subs = (a.block_m + BM - 1) / BM;
+  int mb, strip;
+  unit_tile(blockIdx.x, strips, a.group_m, a.group_n, mb, strip);
+  if (mb >= a.tiles || strip >= strips) return;
+  if constexpr (kMerge) {
+    const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), per = BM / a.block_m;
+    if (mb * per >= nb + min(a.E, nb) * (per - 1)) return;  // (more tiles than these blocks can make)
+    int b = 0, e = 0;
+    const int rows = merged_tile(a, nb, BM, mb, &b, &e);
+    if (rows == 0) return;
+    const int64_t first = (int64_t)b * a.block_m;
+    if (rows > BM / 2) gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, first, rows, e, strip);
+    else gemm_tile<T, MG / 2, NG, WM, WN, kStages + 1>(a, smem, s_slot, first, rows, e, strip);
+  } else {
+    const int b = mb / subs, sub = mb - b * subs;
+    int e = 0;
+    if (a.sorted) {
+      const int nb = *a.ntpp / a.block_m;
+      e = a.eids[b];
+      if (b >= nb || e < 0 || e >= a.E) return;
+    }
+    gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, (int64_t)b * a.block_m + sub * BM,
+                                          min(a.block_m - sub * BM, BM), e, strip);
+  }
 }
 
 template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge = false>
