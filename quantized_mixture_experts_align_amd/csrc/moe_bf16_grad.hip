@@ -333,7 +333,7 @@ extern "C" int moe_bf16_gemm_dgrad(const uint16_t* dC, int64_t ld_dc, const uint
                                    int32_t K, uint16_t* dA, int64_t ld_da, const int32_t* sorted_token_ids,
                                    const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
                                    const int32_t* slot_local_ids, int64_t numel, int32_t top_k, int32_t block_m,
-                                   float* work, int64_t work_elems, hipStream_t stream) {
+                                   int64_t expected_slots, float* work, int64_t work_elems, hipStream_t stream) {
   const char* fn = "moe_bf16_gemm_dgrad";
   int rc = check_grad(fn, dC, ld_dc, E, N, K, numel, top_k, block_m);
   if (rc) return rc;
@@ -353,7 +353,8 @@ extern "C" int moe_bf16_gemm_dgrad(const uint16_t* dC, int64_t ld_dc, const uint
   const BlockGemmArgs a{reinterpret_cast<const uint8_t*>(dC), ld_dc * 2, reinterpret_cast<const uint8_t*>(W), nullptr,
                         0, nullptr, nullptr, top_k == 1 ? static_cast<void*>(dA) : work,
                         top_k == 1 ? ld_da : (int64_t)K, sorted_token_ids, expert_ids, num_tokens_post_padded,
-                        (int32_t)numel, 1, block_m, K, N * 2, E, 0, 0, 0, 0};
+                        (int32_t)numel, 1, block_m, K, N * 2, E, 0, 0, 0, 0,
+                        expected_slots > 0 ? std::min(expected_slots, numel) : numel};
   rc = top_k == 1 ? launch_block_gemm<Bf16TransType<uint16_t>>(fn, a, cap_blocks, stream)
                   : launch_block_gemm<Bf16TransType<float>>(fn, a, cap_blocks, stream);
   if (rc) return rc;

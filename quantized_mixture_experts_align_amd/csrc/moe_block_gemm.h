@@ -37,6 +37,7 @@ struct BlockGemmArgs {
   int32_t numel, top_k, block_m, N, Kb, E;
   int32_t tiles, group_m, group_n;  // tile kernel: tiles of rows; tiles and strips of an XCD's unit
   int32_t cap_blocks;     // most blocks the align can have made
+  int64_t expected;       // live slots to expect: chooses the launch, never a result
 };
 
 struct Fp8Type {
@@ -744,9 +745,9 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
 //   128 x 256, one a CU     6.4 + 1.07 KT us         64 x 64, two a CU    2.8 + 0.51 KT us
 //    64 x 256, one a CU     3.6 + 0.70 KT us
 // and 4 us more for finding the tile's expert and rows.  The rows of routed experts are taken as spread
-// evenly, each expert ending half way through a tile.  256-row tiles are made of an expert's 128-row blocks, counted in the kernel (7 us more), where the
-// batch has 512 slots an expert: with fewer the last, partly filled tile is too large a share (1024
-// Zipf tokens of 8 choices on 32 of 256 experts: 614 us with 128 rows, 655 us with 256).
+// evenly, each expert ending half way through a tile.  256-row tiles are made of an expert's 128-row
+// blocks, counted in the kernel (2 us more), where the batch has 128 slots an expert (1024 Zipf tokens of 8
+// choices on 32 of 256 experts: 618 us with 128 rows, 604 with 256; 4096 of them 975 and 908).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
   if constexpr (!T::kTrans) {
@@ -756,19 +757,20 @@ static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap
       // K = 512 3.8, 3.4, 5.0 us).  Four tiles and two blocks of an expert together where experts have more
       // rows than one block holds often enough (16 slots each on 128 experts, N = K = 2880: 302 -> 245 us;
       // with 2 slots each on 32 experts nothing is gained, 139 and 140 us).
-      const int64_t cus = device_cu_count(), n = (int64_t)((a.N + 31) / 32) * cap_blocks;
+      const int64_t cus = device_cu_count();
+      const int64_t n = (int64_t)((a.N + 31) / 32) * (a.sorted ? std::min<int64_t>(cap_blocks, a.expected) : cap_blocks);
       if (n < cus && a.Kb >= 24 * kStepBytes) return launch_stream<T, 1, 8, 1>(fn, a, cap_blocks, st);
       if (n < 2 * cus) return launch_stream<T, 1, 4, 1>(fn, a, cap_blocks, st);
-      if (a.sorted && a.numel >= 10ll * a.E) return launch_stream<T, 4, 4, 2>(fn, a, cap_blocks, st);
+      if (a.sorted && a.expected >= 10ll * a.E) return launch_stream<T, 4, 4, 2>(fn, a, cap_blocks, st);
       return launch_stream<T, 2, 4, 1>(fn, a, cap_blocks, st);
     }
   }
   const int64_t cus = device_cu_count(), KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   constexpr int64_t kMaxMerged = 4096;  // blocks that every workgroup counts through, 64 at a time
-  const bool merge = a.sorted && a.block_m == 128 && cap_blocks <= kMaxMerged && a.numel >= 512ll * a.E;
+  const bool merge = a.sorted && a.block_m == 128 && cap_blocks <= kMaxMerged && a.expected >= 128ll * a.E;
   auto cost = [&](int BM, int BN, int per_cu, double fixed, double step) {
     const int64_t tiles = a.sorted ? std::min(cap_blocks * ((a.block_m + BM - 1) / BM),
-                                              a.numel / BM + (std::min<int64_t>(a.E, a.numel) + 1) / 2)
+                                              a.expected / BM + (std::min<int64_t>(a.E, a.expected) + 1) / 2)
                                    : ((int64_t)a.numel + BM - 1) / BM;
     const int64_t n = tiles * ((a.N + BN - 1) / BN);
     const double exact = std::max(1.0, (double)n / (double)(cus * per_cu));
@@ -784,7 +786,7 @@ static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap
   const bool rows128 = a.block_m > 64, rows256 = merge || !a.sorted || a.block_m == 256;
   const double low = rows128 ? cost(128, 128, 2, 5.7, 1.18) : never;
   const double mid = rows128 ? cost(128, 256, 1, 6.4, 1.07) : never;
-  const double big = rows256 ? cost(256, 256, 1, merge ? 17.4 : 10.4, 1.68) : never;
+  const double big = rows256 ? cost(256, 256, 1, merge ? 12.4 : 10.4, 1.68) : never;
   const double best = std::min({small, flat, low, mid, big});
   if (big == best) {
     if (merge) return launch_tile<T, 8, 4, 2, 4, 2, true>(fn, a, cap_blocks, st);

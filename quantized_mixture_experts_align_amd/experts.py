@@ -139,10 +139,11 @@ def _w8a8_operands(A, a_scales, W, w_scales, bias, E, N, K) -> None:
 def moe_w8a8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
                   sorted_token_ids: torch.Tensor, expert_ids: torch.Tensor, num_tokens_post_padded: torch.Tensor,
                   numel: int, top_k: int, block_m: int, bias: Optional[torch.Tensor] = None,
-                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  out: Optional[torch.Tensor] = None, expected_slots: int = 0) -> torch.Tensor:
     """C[slot] = W[e] . A[slot // top_k] (+ bias[e]) for the live slots, with A e4m3fn [rows, K] and
     its scales [rows, ceil(K/128)] (moe_fp8_quant), W e4m3fn [E, N, K] and its scales
-    [E, ceil(N/128), ceil(K/128)]; C is bf16 [numel, N]."""
+    [E, ceil(N/128), ceil(K/128)]; C is bf16 [numel, N].  expected_slots: slots expected to be live on
+    this slice (0: all), a launch hint."""
     _check(A, "A", _F8, rows=True)
     if W.dim() != 3:
         raise ValueError(f"W must be [E, N, K], got {tuple(W.shape)}")
@@ -157,7 +158,8 @@ def moe_w8a8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_sc
         _check(out, "out", _BF16, (numel, N), A.device, rows=True)
     _call(A.device, "moe_w8a8_gemm", A.data_ptr(), A.shape[0], _ld(A), a_scales.data_ptr(), _ld(a_scales), W.data_ptr(),
           w_scales.data_ptr(), None if bias is None else bias.data_ptr(), E, N, K, out.data_ptr(), _ld(out),
-          sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), numel, top_k, block_m)
+          sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), numel, top_k, block_m,
+          expected_slots)
     return out
 
 
@@ -182,9 +184,10 @@ def moe_w8a8_linear(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_
 
 def moe_bf16_gemm(A: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tensor, expert_ids: torch.Tensor,
                   num_tokens_post_padded: torch.Tensor, numel: int, top_k: int, block_m: int,
-                  bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  expected_slots: int = 0) -> torch.Tensor:
     """C[slot] = W[e] . A[slot // top_k] (+ bias[e]) for the live slots: A bf16 [rows, K], W bf16
-    [E, N, K], bias bf16 [E, N]; C is bf16 [numel, N]."""
+    [E, N, K], bias bf16 [E, N]; C is bf16 [numel, N].  expected_slots as moe_w8a8_gemm."""
     _check(A, "A", _BF16, rows=True)
     if W.dim() != 3 or W.shape[2] != A.shape[1]:
         raise ValueError(f"W {tuple(W.shape)} must be [E, N, K] with the {A.shape[1]} columns of A")
@@ -197,22 +200,23 @@ def moe_bf16_gemm(A: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tens
         out = torch.empty((numel, N), dtype=torch.bfloat16, device=dev)
     else:
         _check(out, "out", _BF16, (numel, N), dev, rows=True)
-    _bf16_gemm(A, W, sorted_token_ids, expert_ids, num_tokens_post_padded, numel, top_k, block_m, bias, out)
+    _bf16_gemm(A, W, sorted_token_ids, expert_ids, num_tokens_post_padded, numel, top_k, block_m, bias, out,
+               expected_slots)
     return out
 
 
 # (the calls proper, for tensors that have been checked)
-def _bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, numel, top_k, block_m, bias, out) -> None:
+def _bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, numel, top_k, block_m, bias, out, expected) -> None:
     E, N, K = W.shape
     _call(A.device, "moe_bf16_gemm", A.data_ptr(), A.shape[0], _ld(A), W.data_ptr(),
           None if bias is None else bias.data_ptr(), E, N, K, out.data_ptr(), _ld(out), sorted_ids.data_ptr(),
-          expert_ids.data_ptr(), ntpp.data_ptr(), numel, top_k, block_m)
+          expert_ids.data_ptr(), ntpp.data_ptr(), numel, top_k, block_m, expected)
 
 
-def _dgrad(dC, W, sorted_ids, expert_ids, ntpp, live: int, top_k, block_m, out, work) -> None:
+def _dgrad(dC, W, sorted_ids, expert_ids, ntpp, live: int, top_k, block_m, out, work, expected) -> None:
     E, N, K = W.shape
     _call(dC.device, "moe_bf16_gemm_dgrad", dC.data_ptr(), _ld(dC), W.data_ptr(), E, N, K, out.data_ptr(), _ld(out),
-          sorted_ids.data_ptr(), expert_ids.data_ptr(), ntpp.data_ptr(), live, dC.shape[0], top_k, block_m,
+          sorted_ids.data_ptr(), expert_ids.data_ptr(), ntpp.data_ptr(), live, dC.shape[0], top_k, block_m, expected,
           None if work is None else work.data_ptr(), 0 if work is None else work.numel())
 
 
@@ -224,10 +228,11 @@ def _wgrad(dC, A, E, sorted_ids, expert_ids, ntpp, top_k, block_m, out, out_bias
 
 def moe_bf16_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tensor, expert_ids: torch.Tensor,
                         num_tokens_post_padded: torch.Tensor, slot_local_ids: torch.Tensor, top_k: int, block_m: int,
-                        out: Optional[torch.Tensor] = None, work: Optional[torch.Tensor] = None) -> torch.Tensor:
+                        out: Optional[torch.Tensor] = None, work: Optional[torch.Tensor] = None,
+                        expected_slots: int = 0) -> torch.Tensor:
     """Gradient of moe_bf16_gemm with respect to A: dC bf16 [numel, N], W bf16 [E, N, K] -> bf16
     [numel // top_k, K], zero in rows without a live slot.  `work`: float32 workspace of numel * K
-    values for top_k > 1 (allocated when not given)."""
+    values for top_k > 1 (allocated when not given).  expected_slots as moe_w8a8_gemm."""
     _check(dC, "dC", _BF16, rows=True)
     dev, numel = dC.device, dC.shape[0]
     if W.dim() != 3 or W.shape[1] != dC.shape[1]:
@@ -251,7 +256,8 @@ def moe_bf16_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, sorted_token_ids: tor
             _check(work, "work", _F32, dev=dev)
     else:
         work = None
-    _dgrad(dC, W, sorted_token_ids, expert_ids, num_tokens_post_padded, live, top_k, block_m, out, work)
+    _dgrad(dC, W, sorted_token_ids, expert_ids, num_tokens_post_padded, live, top_k, block_m, out, work,
+           expected_slots)
     return out
 
 
@@ -295,11 +301,12 @@ def moe_zero_dropped_rows(C: torch.Tensor, slot_local_ids: torch.Tensor) -> torc
 
 class _ExpertsLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, A, W, bias, sorted_ids, expert_ids, ntpp, slot_local, top_k, block_m):
-        out = moe_bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, slot_local.numel(), top_k, block_m, bias=bias)
+    def forward(ctx, A, W, bias, sorted_ids, expert_ids, ntpp, slot_local, top_k, block_m, expected):
+        out = moe_bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, slot_local.numel(), top_k, block_m, bias=bias,
+                            expected_slots=expected)
         moe_zero_dropped_rows(out, slot_local)
         ctx.save_for_backward(A, W, sorted_ids, expert_ids, ntpp, slot_local)
-        ctx.top_k, ctx.block_m, ctx.has_bias = top_k, block_m, bias is not None
+        ctx.top_k, ctx.block_m, ctx.expected, ctx.has_bias = top_k, block_m, expected, bias is not None
         return out
 
     @staticmethod
@@ -313,27 +320,28 @@ class _ExpertsLinear(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             dA = torch.empty(A.shape, dtype=A.dtype, device=A.device)
             work = None if ctx.top_k == 1 else torch.empty(grad.shape[0] * W.shape[2], dtype=torch.float32, device=A.device)
-            _dgrad(grad, W, *align, slot_local.data_ptr(), ctx.top_k, ctx.block_m, dA, work)
+            _dgrad(grad, W, *align, slot_local.data_ptr(), ctx.top_k, ctx.block_m, dA, work, ctx.expected)
         if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
             dW = torch.empty_like(W)
             if ctx.has_bias and ctx.needs_input_grad[2]:
                 db = torch.empty(W.shape[:2], dtype=W.dtype, device=W.device)
             _wgrad(grad, A, W.shape[0], *align, ctx.top_k, ctx.block_m, dW, db)
-        return dA, dW, db, None, None, None, None, None, None
+        return dA, dW, db, None, None, None, None, None, None, None
 
 
 def moe_experts_linear(A: torch.Tensor, W: torch.Tensor, align, top_k: int, block_m: int,
-                       bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+                       bias: Optional[torch.Tensor] = None, expected_slots: int = 0) -> torch.Tensor:
     """Differentiable moe_bf16_gemm: C bf16 [numel, N] with C[slot] = W[e] . A[slot // top_k]
     (+ bias[e]) and zeros in the rows of dropped slots.
 
     `align` is what moe_align returns for the batch (sorted_token_ids, expert_ids,
     num_tokens_post_padded, slot_local_ids) with the same block_m; A has numel // top_k rows (one
     for each token with the layer's top_k, or one for each slot with top_k = 1).  Gradients flow to
-    A, W and bias; they are bf16, once differentiable, and zero for rows and experts without slots."""
+    A, W and bias; they are bf16, once differentiable, and zero for rows and experts without slots.
+    expected_slots as moe_w8a8_gemm."""
     sorted_ids, expert_ids, ntpp, slot_local = align
     if slot_local is None:
         raise ValueError("moe_experts_linear needs the align's slot_local_ids")
     if top_k < 1 or A.dim() != 2 or A.shape[0] * top_k != slot_local.numel():
         raise ValueError(f"A {tuple(A.shape)} must have a row for each {top_k} of the {slot_local.numel()} slots")
-    return _ExpertsLinear.apply(A, W, bias, sorted_ids, expert_ids, ntpp, slot_local, top_k, block_m)
+    return _ExpertsLinear.apply(A, W, bias, sorted_ids, expert_ids, ntpp, slot_local, top_k, block_m, expected_slots)

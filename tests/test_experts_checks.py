@@ -10,13 +10,13 @@ from quantized_mixture_experts_align_amd import _lib as L
 A16 = 0x10000          # an aligned address
 QUANT = dict(x=A16, ld_x=256, R=4, K=256, live=None, codes=A16, ld_codes=256, scales=A16, ld_scales=2, stream=None)
 W8A8 = dict(A=A16, a_rows=8, lda=256, a_scales=A16, ld_scales=2, W=A16, w_scales=A16, bias=None, E=4, N=128, K=256,
-            C=A16, ldc=128, sorted=A16, eids=A16, ntpp=A16, numel=16, top_k=2, block_m=16, stream=None)
+            C=A16, ldc=128, sorted=A16, eids=A16, ntpp=A16, numel=16, top_k=2, block_m=16, expected=0, stream=None)
 LINEAR = dict(A=A16, M=8, lda=256, a_scales=A16, ld_scales=2, W=A16, w_scales=A16, bias=None, N=128, K=256, C=A16,
               ldc=128, stream=None)
 BF16 = dict(A=A16, a_rows=8, lda=256, W=A16, bias=None, E=4, N=128, K=256, C=A16, ldc=128, sorted=A16, eids=A16,
-            ntpp=A16, numel=16, top_k=2, block_m=16, stream=None)
+            ntpp=A16, numel=16, top_k=2, block_m=16, expected=0, stream=None)
 DGRAD = dict(dC=A16, ld_dc=128, W=A16, E=4, N=128, K=256, dA=A16, ld_da=256, sorted=A16, eids=A16, ntpp=A16, live=A16,
-             numel=16, top_k=2, block_m=16, work=A16, work_elems=16 * 256, stream=None)
+             numel=16, top_k=2, block_m=16, expected=0, work=A16, work_elems=16 * 256, stream=None)
 WGRAD = dict(dC=A16, ld_dc=128, A=A16, a_rows=8, lda=256, E=4, N=128, K=256, dW=A16, dbias=None, f32=0, sorted=A16,
              eids=A16, ntpp=A16, numel=16, top_k=2, block_m=16, stream=None)
 ZERO = dict(live=A16, rows=4, N=128, C=A16, ldc=128, stream=None)

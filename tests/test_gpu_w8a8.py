@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 NANS = 0x7F
 
 
-def case(M, k, E_all, E, N, K, B, top_k, bias, seed, start=0, only=None, pad=0):
+def case(M, k, E_all, E, N, K, B, top_k, bias, seed, start=0, only=None, pad=0, expected=0):
     ids = routing(M, k, E_all, E, seed, only)
     al, local = aligned(ids, start, E, B)
     rows = M if top_k == k else M * k
@@ -24,7 +24,7 @@ def case(M, k, E_all, E, N, K, B, top_k, bias, seed, start=0, only=None, pad=0):
     base = torch.full((M * k, N + (8 if pad else 0)), -5.0, dtype=torch.bfloat16, device="cuda")
     out = base[:, :N]
     got = P.moe_w8a8_gemm(A, SA, w.cuda(), sb.cuda(), *al[:3], M * k, top_k, B, bias=None if b is None else b.cuda(),
-                          out=out)
+                          out=out, expected_slots=expected)
     assert got is out
     dead = local < 0
     assert bool((base[torch.from_numpy(dead).cuda()] == -5.0).all()) and bool((base[:, N:] == -5.0).all())
@@ -55,6 +55,12 @@ def test_tiles_of_several_blocks(M, k, E, N, K, B):
     r = np.random.default_rng(M)
     case(M, k, 2 * E, E, N, K, B, k, True, M, only=r.choice(2 * E, size=max(k, E), replace=False))
     case(M, k, E, E, N, K, B, 1, False, M + 1, only=[E - 1] if k == 1 else None)
+
+
+@pytest.mark.parametrize("B", [16, 32, 128])
+@pytest.mark.parametrize("expected", [1, 40, 100000])
+def test_the_launch_hint_changes_no_result(B, expected):
+    case(130, 4, 5, 5, 520, 656, B, 4, False, 70 + B, expected=expected)
 
 
 @pytest.mark.parametrize("B", [16, 64, 128])
