@@ -12,7 +12,7 @@ from .ops import (align_capacity, choose_block_m, gemm_choose, gemm_occupancy, g
                   moe_w4a16_gemm_combine, combine_counters,
                   moe_w4a16_gemm_combine_noalloc)
 from .experts import (moe_act_fp8_quant, moe_bf16_gemm, moe_bf16_gemm_dgrad, moe_bf16_gemm_wgrad, moe_experts_linear,
-                      moe_fp8_quant, moe_w8a8_gemm, moe_w8a8_linear, moe_zero_dropped_rows)
+                      moe_fp8_quant, moe_w8a8_gemm, moe_w8a8_linear)
 from .layer import MoELayer, Workspace
 
 __all__ = [
@@ -23,5 +23,5 @@ __all__ = [
     "requant_config", "moe_permute_cols", "moe_w4a16_gemm_combine", "combine_counters",
     "moe_w4a16_gemm_combine_noalloc", "moe_fp8_quant", "moe_act_fp8_quant", "moe_w8a8_gemm",
     "moe_w8a8_linear", "moe_bf16_gemm", "moe_bf16_gemm_dgrad", "moe_bf16_gemm_wgrad",
-    "moe_zero_dropped_rows", "moe_experts_linear",
+    "moe_experts_linear",
 ]

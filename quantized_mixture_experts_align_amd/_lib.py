@@ -82,13 +82,12 @@ SIGNATURES = {
     "moe_w8a8_gemm": (C.c_int, [_P, _I64, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _P, _I64, _P, _P, _P,
                                 _I64, _I32, _I32, _I64, _P]),
     "moe_w8a8_linear": (C.c_int, [_P, _I64, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _P, _I64, _P]),
-    "moe_bf16_gemm": (C.c_int, [_P, _I64, _I64, _P, _P, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _I64, _I32,
-                                _I32, _I64, _P]),
+    "moe_bf16_gemm": (C.c_int, [_P, _I64, _I64, _P, _P, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I64,
+                                _I32, _I32, _I64, _P]),
     "moe_bf16_gemm_dgrad": (C.c_int, [_P, _I64, _P, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I64, _I32,
                                       _I32, _I64, _P, _I64, _P]),
     "moe_bf16_gemm_wgrad": (C.c_int, [_P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P,
                                       _I64, _I32, _I32, _P]),
-    "moe_zero_dropped_rows": (C.c_int, [_P, _I64, _I32, _P, _I64, _P]),
 }
 
 _lib = None

@@ -256,16 +256,6 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
   }
 }
 
-// zeros in the rows of dropped slots (the others are not touched)
-__global__ __launch_bounds__(256) void zero_dead_kernel(const int32_t* __restrict__ live, int64_t rows, int32_t K,
-                                                        uint16_t* __restrict__ dst, int64_t ld) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    if (live[r] >= 0) continue;
-    for (int c = threadIdx.x * 8; c < K; c += 256 * 8)
-      *reinterpret_cast<u32x4_t*>(dst + r * ld + c) = u32x4_t{0u, 0u, 0u, 0u};
-  }
-}
-
 template <typename OUT, int MG, int NG, int WM, int WN, int kStages>
 static int launch_wgrad_tile(const char* fn, GradArgs a, hipStream_t st) {
   constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
@@ -289,13 +279,6 @@ static int launch_wgrad(const char* fn, const GradArgs& a, hipStream_t st) {
   return launch_wgrad_tile<OUT, 4, 2, 2, 4, 2>(fn, a, st);
 }
 
-static int zero_dead(const char* fn, const int32_t* live, int64_t rows, int32_t K, uint16_t* dst, int64_t ld,
-                     hipStream_t st) {
-  hipLaunchKernelGGL(zero_dead_kernel, dim3((unsigned)std::min<int64_t>(rows, 4096)), dim3(256), 0, st, live, rows, K,
-                     dst, ld);
-  return check_launch(fn);
-}
-
 static int check_grad(const char* fn, const void* dC, int64_t ld_dc, int32_t E, int32_t N, int32_t K, int64_t numel,
                       int32_t top_k, int32_t block_m) {
   MOE_REQUIRE(E >= 1 && N >= 1 && K >= 1, MOE_EINVAL, "%s: E=%d N=%d K=%d", fn, E, N, K);
@@ -316,18 +299,6 @@ static int check_grad(const char* fn, const void* dC, int64_t ld_dc, int32_t E, 
 }  // namespace moe
 
 using namespace moe;
-
-extern "C" int moe_zero_dropped_rows(const int32_t* slot_local_ids, int64_t rows, int32_t N, uint16_t* C, int64_t ldc,
-                                     hipStream_t stream) {
-  const char* fn = "moe_zero_dropped_rows";
-  MOE_REQUIRE(rows >= 0 && N >= 1, MOE_EINVAL, "%s: rows=%lld N=%d", fn, (long long)rows, N);
-  MOE_REQUIRE(N % 8 == 0 && ldc >= N && ldc % 8 == 0, MOE_EUNSUPPORTED,
-              "%s: N=%d and ldc=%lld must be multiples of 8, ldc >= N", fn, N, (long long)ldc);
-  if (rows == 0) return ok();
-  MOE_REQUIRE(slot_local_ids && C, MOE_EINVAL, "%s: null pointer", fn);
-  MOE_REQUIRE(((uintptr_t)C & 15) == 0, MOE_EUNSUPPORTED, "%s: misaligned pointer (16 B)", fn);
-  return zero_dead(fn, slot_local_ids, rows, N, C, ldc, stream);
-}
 
 extern "C" int moe_bf16_gemm_dgrad(const uint16_t* dC, int64_t ld_dc, const uint16_t* W, int32_t E, int32_t N,
                                    int32_t K, uint16_t* dA, int64_t ld_da, const int32_t* sorted_token_ids,
@@ -353,12 +324,11 @@ extern "C" int moe_bf16_gemm_dgrad(const uint16_t* dC, int64_t ld_dc, const uint
   const BlockGemmArgs a{reinterpret_cast<const uint8_t*>(dC), ld_dc * 2, reinterpret_cast<const uint8_t*>(W), nullptr,
                         0, nullptr, nullptr, top_k == 1 ? static_cast<void*>(dA) : work,
                         top_k == 1 ? ld_da : (int64_t)K, sorted_token_ids, expert_ids, num_tokens_post_padded,
-                        (int32_t)numel, 1, block_m, K, N * 2, E, 0, 0, 0, 0,
+                        (int32_t)numel, 1, block_m, K, N * 2, E, 0, 0, 0, 0, top_k == 1 ? slot_local_ids : nullptr,
                         expected_slots > 0 ? std::min(expected_slots, numel) : numel};
   rc = top_k == 1 ? launch_block_gemm<Bf16TransType<uint16_t>>(fn, a, cap_blocks, stream)
                   : launch_block_gemm<Bf16TransType<float>>(fn, a, cap_blocks, stream);
-  if (rc) return rc;
-  if (top_k == 1) return zero_dead(fn, slot_local_ids, numel, K, dA, ld_da, stream);
+  if (rc || top_k == 1) return rc;  // (rows of dropped slots are zeroed by the same launch)
   hipLaunchKernelGGL(sum_slots_kernel, dim3((unsigned)(numel / top_k)), dim3(256), 0, stream, work,
                      slot_local_ids, top_k, K, dA, ld_da);
   return check_launch(fn);

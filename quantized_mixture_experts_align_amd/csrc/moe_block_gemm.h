@@ -37,6 +37,7 @@ struct BlockGemmArgs {
   int32_t numel, top_k, block_m, N, Kb, E;
   int32_t tiles, group_m, group_n;  // tile kernel: tiles of rows; tiles and strips of an XCD's unit
   int32_t cap_blocks;     // most blocks the align can have made
+  const int32_t* live;    // set: rows of C whose slot is dropped (live[slot] < 0) are zeroed, else left alone
   int64_t expected;       // live slots to expect: chooses the launch, never a result
 };
 
@@ -100,15 +101,38 @@ __device__ __forceinline__ int slot_at(const BlockGemmArgs& a, int64_t at) {
   return s >= 0 && s < a.numel ? (int)s : -1;
 }
 
+// Zeros in the rows of dropped slots, shared by all the workgroups of a launch: rows blockIdx.x, +
+// gridDim.x, ..., of which `mine` holds the flags of the first 64 (asked for when the workgroup starts,
+// as drop_flags, so that its end does not wait for them).
+__device__ __forceinline__ int drop_flags(const BlockGemmArgs& a, int64_t first) {
+  const int64_t r = first + (int64_t)gridDim.x * (threadIdx.x & 63);
+  return a.live && r < a.numel ? a.live[r] : 0;
+}
+template <typename OUT>
+__device__ __forceinline__ void zero_dropped(const BlockGemmArgs& a, int mine) {
+  if (!a.live) return;
+  for (int64_t first = blockIdx.x;;) {
+    for (uint64_t dead = __ballot(mine < 0); dead; dead &= dead - 1) {
+      OUT* row = static_cast<OUT*>(a.C) + (first + (int64_t)gridDim.x * __builtin_ctzll(dead)) * a.ldc;
+      for (int c = threadIdx.x * 4; c < a.N; c += blockDim.x * 4) {
+        if constexpr (sizeof(OUT) == 4) *reinterpret_cast<f32x4_t*>(row + c) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        else *reinterpret_cast<u32x2_t*>(row + c) = u32x2_t{0u, 0u};
+      }
+    }
+    first += (int64_t)gridDim.x * 64;
+    if (first >= a.numel) break;
+    mine = drop_flags(a, first);
+  }
+}
+
 // ---------------------------------------------------------------------------- few rows
 // Workgroup = up to 16 slots of a block (MB = 2: of two consecutive blocks of one expert) x NG 16-row
 // weight tiles, K split over its KS waves, operands straight from memory to registers in chunks of
 // kChunk steps, partial sums joined through LDS in wave order.  The cost is the stream of weights (64 tokens of 8 choices on 32 of 256
 // experts, N = 8192, K = 4096: 139 us, 6.7 TB/s).
 template <typename T, int NG, int KS, int MB>
-__global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArgs a) {
+__device__ __forceinline__ void gemm_stream(const BlockGemmArgs& a, f32x4_t (&part)[KS][NG * MB][64]) {
   constexpr int kChunk = 4;
-  __shared__ f32x4_t part[KS][NG * MB][64];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int strips = (a.N + 16 * NG - 1) / (16 * NG);
   const int strip = blockIdx.x % strips, b = blockIdx.x / strips;
@@ -226,6 +250,14 @@ __global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArg
           u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
   }
+}
+
+template <typename T, int NG, int KS, int MB>
+__global__ __launch_bounds__(64 * KS) void block_gemm_stream_kernel(BlockGemmArgs a) {
+  __shared__ f32x4_t part[KS][NG * MB][64];
+  const int flags = T::kScaled ? 0 : drop_flags(a, blockIdx.x);
+  gemm_stream<T, NG, KS, MB>(a, part);
+  if constexpr (!T::kScaled) zero_dropped<uint16_t>(a, flags);
 }
 
 template <typename T, int NG, int KS, int MB>
@@ -688,30 +720,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
   constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
   __shared__ __attribute__((aligned(128))) uint8_t smem[tile_bytes<T, MG, NG, WM, WN, kStages, kMerge>()];
   __shared__ int s_slot[BM];
-  const int strips = (a.N + BN - 1) / BN, subs = (a.block_m + BM - 1) / BM;
-  int mb, strip;
-  unit_tile(blockIdx.x, strips, a.group_m, a.group_n, mb, strip);
-  if (mb >= a.tiles || strip >= strips) return;
-  if constexpr (kMerge) {
-    const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), per = BM / a.block_m;
-    if (mb * per >= nb + min(a.E, nb) * (per - 1)) return;  // (more tiles than these blocks can make)
-    int b = 0, e = 0;
-    const int rows = merged_tile(a, nb, BM, mb, &b, &e);
-    if (rows == 0) return;
-    const int64_t first = (int64_t)b * a.block_m;
-    if (rows > BM / 2) gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, first, rows, e, strip);
-    else gemm_tile<T, MG / 2, NG, WM, WN, kStages + 1>(a, smem, s_slot, first, rows, e, strip);
-  } else {
-    const int b = mb / subs, sub = mb - b * subs;
-    int e = 0;
-    if (a.sorted) {
-      const int nb = *a.ntpp / a.block_m;
-      e = a.eids[b];
-      if (b >= nb || e < 0 || e >= a.E) return;
+  const int flags = T::kScaled ? 0 : drop_flags(a, blockIdx.x);
+  auto work = [&]() __attribute__((always_inline)) {
+    const int strips = (a.N + BN - 1) / BN, subs = (a.block_m + BM - 1) / BM;
+    int mb, strip;
+    unit_tile(blockIdx.x, strips, a.group_m, a.group_n, mb, strip);
+    if (mb >= a.tiles || strip >= strips) return;
+    if constexpr (kMerge) {
+      const int nb = min(*a.ntpp / a.block_m, a.cap_blocks), per = BM / a.block_m;
+      if (mb * per >= nb + min(a.E, nb) * (per - 1)) return;  // (more tiles than these blocks can make)
+      int b = 0, e = 0;
+      const int rows = merged_tile(a, nb, BM, mb, &b, &e);
+      if (rows == 0) return;
+      const int64_t first = (int64_t)b * a.block_m;
+      if (rows > BM / 2) gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, first, rows, e, strip);
+      else gemm_tile<T, MG / 2, NG, WM, WN, kStages + 1>(a, smem, s_slot, first, rows, e, strip);
+    } else {
+      const int b = mb / subs, sub = mb - b * subs;
+      int e = 0;
+      if (a.sorted) {
+        const int nb = *a.ntpp / a.block_m;
+        e = a.eids[b];
+        if (b >= nb || e < 0 || e >= a.E) return;
+      }
+      gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, (int64_t)b * a.block_m + sub * BM,
+                                            min(a.block_m - sub * BM, BM), e, strip);
     }
-    gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, (int64_t)b * a.block_m + sub * BM,
-                                          min(a.block_m - sub * BM, BM), e, strip);
-  }
+  };
+  work();
+  if constexpr (!T::kScaled) zero_dropped<typename T::Out>(a, flags);
 }
 
 template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge = false>

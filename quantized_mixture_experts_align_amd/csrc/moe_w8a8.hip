@@ -22,7 +22,7 @@ static int w8a8(const char* fn, bool dense, const uint8_t* A, int64_t a_rows, in
     if (rc) return rc;
   }
   const BlockGemmArgs a{A, lda, W, a_scales, ld_as, w_scales, bias, C, ldc, dense ? nullptr : sorted, eids, ntpp,
-                        (int32_t)numel, top_k, block_m, N, K, E, 0, 0, 0, 0,
+                        (int32_t)numel, top_k, block_m, N, K, E, 0, 0, 0, 0, nullptr,
                         expected > 0 ? std::min(expected, numel) : numel};
   return launch_block_gemm<Fp8Type>(fn, a, cap_blocks, stream);
 }

@@ -185,9 +185,10 @@ def moe_w8a8_linear(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_
 def moe_bf16_gemm(A: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tensor, expert_ids: torch.Tensor,
                   num_tokens_post_padded: torch.Tensor, numel: int, top_k: int, block_m: int,
                   bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                  expected_slots: int = 0) -> torch.Tensor:
+                  expected_slots: int = 0, slot_local_ids: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C[slot] = W[e] . A[slot // top_k] (+ bias[e]) for the live slots: A bf16 [rows, K], W bf16
-    [E, N, K], bias bf16 [E, N]; C is bf16 [numel, N].  expected_slots as moe_w8a8_gemm."""
+    [E, N, K], bias bf16 [E, N]; C is bf16 [numel, N].  With slot_local_ids the rows of dropped slots are
+    zeroed, without they are left as they are.  expected_slots as moe_w8a8_gemm."""
     _check(A, "A", _BF16, rows=True)
     if W.dim() != 3 or W.shape[2] != A.shape[1]:
         raise ValueError(f"W {tuple(W.shape)} must be [E, N, K] with the {A.shape[1]} columns of A")
@@ -201,16 +202,16 @@ def moe_bf16_gemm(A: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tens
     else:
         _check(out, "out", _BF16, (numel, N), dev, rows=True)
     _bf16_gemm(A, W, sorted_token_ids, expert_ids, num_tokens_post_padded, numel, top_k, block_m, bias, out,
-               expected_slots)
+               expected_slots, _live_ptr(slot_local_ids, numel, dev))
     return out
 
 
 # (the calls proper, for tensors that have been checked)
-def _bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, numel, top_k, block_m, bias, out, expected) -> None:
+def _bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, numel, top_k, block_m, bias, out, expected, live) -> None:
     E, N, K = W.shape
     _call(A.device, "moe_bf16_gemm", A.data_ptr(), A.shape[0], _ld(A), W.data_ptr(),
           None if bias is None else bias.data_ptr(), E, N, K, out.data_ptr(), _ld(out), sorted_ids.data_ptr(),
-          expert_ids.data_ptr(), ntpp.data_ptr(), numel, top_k, block_m, expected)
+          expert_ids.data_ptr(), ntpp.data_ptr(), live, numel, top_k, block_m, expected)
 
 
 def _dgrad(dC, W, sorted_ids, expert_ids, ntpp, live: int, top_k, block_m, out, work, expected) -> None:
@@ -290,21 +291,11 @@ def moe_bf16_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, n_experts: int, sorte
     return out, out_bias
 
 
-def moe_zero_dropped_rows(C: torch.Tensor, slot_local_ids: torch.Tensor) -> torch.Tensor:
-    """Zeros, in place, in the rows of C (bf16 [numel, N]) whose slot is dropped."""
-    _check(C, "C", _BF16, rows=True)
-    _check(slot_local_ids, "slot_local_ids", _I32, dev=C.device)
-    live = _live_ptr(slot_local_ids, C.shape[0], C.device)
-    _call(C.device, "moe_zero_dropped_rows", live, C.shape[0], C.shape[1], C.data_ptr(), _ld(C))
-    return C
-
-
 class _ExpertsLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, A, W, bias, sorted_ids, expert_ids, ntpp, slot_local, top_k, block_m, expected):
         out = moe_bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, slot_local.numel(), top_k, block_m, bias=bias,
-                            expected_slots=expected)
-        moe_zero_dropped_rows(out, slot_local)
+                            expected_slots=expected, slot_local_ids=slot_local)
         ctx.save_for_backward(A, W, sorted_ids, expert_ids, ntpp, slot_local)
         ctx.top_k, ctx.block_m, ctx.expected, ctx.has_bias = top_k, block_m, expected, bias is not None
         return out

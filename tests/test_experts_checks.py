@@ -14,12 +14,11 @@ W8A8 = dict(A=A16, a_rows=8, lda=256, a_scales=A16, ld_scales=2, W=A16, w_scales
 LINEAR = dict(A=A16, M=8, lda=256, a_scales=A16, ld_scales=2, W=A16, w_scales=A16, bias=None, N=128, K=256, C=A16,
               ldc=128, stream=None)
 BF16 = dict(A=A16, a_rows=8, lda=256, W=A16, bias=None, E=4, N=128, K=256, C=A16, ldc=128, sorted=A16, eids=A16,
-            ntpp=A16, numel=16, top_k=2, block_m=16, expected=0, stream=None)
+            ntpp=A16, live=None, numel=16, top_k=2, block_m=16, expected=0, stream=None)
 DGRAD = dict(dC=A16, ld_dc=128, W=A16, E=4, N=128, K=256, dA=A16, ld_da=256, sorted=A16, eids=A16, ntpp=A16, live=A16,
              numel=16, top_k=2, block_m=16, expected=0, work=A16, work_elems=16 * 256, stream=None)
 WGRAD = dict(dC=A16, ld_dc=128, A=A16, a_rows=8, lda=256, E=4, N=128, K=256, dW=A16, dbias=None, f32=0, sorted=A16,
              eids=A16, ntpp=A16, numel=16, top_k=2, block_m=16, stream=None)
-ZERO = dict(live=A16, rows=4, N=128, C=A16, ldc=128, stream=None)
 
 BAD = [
     ("moe_fp8_quant", QUANT, L.MOE_EINVAL, [dict(x=None), dict(codes=None), dict(scales=None), dict(R=-1), dict(K=0),
@@ -55,8 +54,6 @@ BAD = [
                                                   dict(numel=17), dict(ld_dc=64), dict(top_k=0)]),
     ("moe_bf16_gemm_wgrad", WGRAD, L.MOE_EUNSUPPORTED, [dict(A=A16 + 8), dict(dW=A16 + 8), dict(dbias=A16 + 2),
                                                         dict(K=260, lda=264), dict(E=513)]),
-    ("moe_zero_dropped_rows", ZERO, L.MOE_EINVAL, [dict(live=None), dict(C=None), dict(rows=-1), dict(N=0)]),
-    ("moe_zero_dropped_rows", ZERO, L.MOE_EUNSUPPORTED, [dict(N=124), dict(ldc=132), dict(C=A16 + 8), dict(ldc=120)]),
 ]
 
 
@@ -83,8 +80,7 @@ def test_empty_batches_launch_nothing():
                                ("moe_w8a8_gemm", W8A8, dict(numel=0, A=None, C=None, sorted=None)),
                                ("moe_w8a8_linear", LINEAR, dict(M=0, A=None)),
                                ("moe_bf16_gemm", BF16, dict(numel=0, A=None)),
-                               ("moe_bf16_gemm_dgrad", DGRAD, dict(numel=0, dC=None, dA=None, work_elems=0)),
-                               ("moe_zero_dropped_rows", ZERO, dict(rows=0, C=None))):
+                               ("moe_bf16_gemm_dgrad", DGRAD, dict(numel=0, dC=None, dA=None, work_elems=0))):
         assert getattr(L.lib(), name)(*{**good, **change}.values()) == L.MOE_OK, name
 
 
@@ -95,7 +91,7 @@ def test_host_tensors_are_refused():
     for call in (lambda: P.moe_fp8_quant(x), lambda: P.moe_act_fp8_quant("relu2", x, 128),
                  lambda: P.moe_w8a8_linear(q, s, q, s), lambda: P.moe_w8a8_gemm(q, s, w, s, i, i, i, 4, 1, 16),
                  lambda: P.moe_bf16_gemm(x, w, i, i, i, 4, 1, 16), lambda: P.moe_bf16_gemm_dgrad(x, w, i, i, i, i, 1, 16),
-                 lambda: P.moe_bf16_gemm_wgrad(x, x, 1, i, i, i, 1, 16), lambda: P.moe_zero_dropped_rows(x, i[:4])):
+                 lambda: P.moe_bf16_gemm_wgrad(x, x, 1, i, i, i, 1, 16)):
         with pytest.raises(ValueError, match="device tensor"):
             call()
 

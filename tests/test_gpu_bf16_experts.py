@@ -52,7 +52,7 @@ def test_product_and_gradients(M, k, E, N, K, B, gather):
     P.moe_bf16_gemm(A, W, *al[:3], M * k, top_k, B, bias=b.cuda(), out=out)
     dead = torch.from_numpy(local < 0).cuda()
     assert bool((out[dead] == -5.0).all())
-    P.moe_zero_dropped_rows(out, al[3])
+    P.moe_bf16_gemm(A, W, *al[:3], M * k, top_k, B, bias=b.cuda(), out=out, slot_local_ids=al[3])
     assert_close(out, want, bound + U16 * np.abs(want) + 1e-30, "C")
     dA, dW, db = gradients(G64, A64, W64, local, top_k)
     got = P.moe_bf16_gemm_dgrad(G, W, *al, top_k, B)
