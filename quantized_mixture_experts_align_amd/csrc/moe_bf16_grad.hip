@@ -26,219 +26,256 @@ struct GradArgs {
   const int32_t* ntpp;
   int32_t numel, top_k, block_m, N, K, E;
   int32_t cap_blocks;  // most blocks the align can have made
-  int32_t group_m, group_n;
+  int32_t group_m, group_n, positions;
   uint32_t div_mul, div_shift;  // s / top_k for 0 <= s < 2^31 (top_k > 1)
   __device__ __forceinline__ uint32_t row_of(uint32_t s) const {
     return top_k == 1 ? s : __umulhi(s, div_mul) >> div_shift;
   }
 };
 
-// [first, last) of the sorted entries of expert e: the align lists the experts' blocks in rising
-// order (and -1 behind them), so counting the blocks of lower and of equal experts gives its range.
-// Every thread of the workgroup calls it; `red` holds two ints for each wave.
-__device__ __forceinline__ void expert_range(const GradArgs& a, int e, int* red, int64_t* first, int64_t* last) {
-  const int lane = threadIdx.x & 63;
-  int lower = 0, equal = 0;
-  for (int i = threadIdx.x; i < a.cap_blocks; i += blockDim.x) {
-    const int v = a.eids[i];
-    lower += v >= 0 && v < e;
-    equal += v == e;
-  }
-  for (int d = 32; d >= 1; d >>= 1) {
-    lower += __shfl_xor(lower, d);
-    equal += __shfl_xor(equal, d);
-  }
-  if (lane == 0) {
-    red[2 * (threadIdx.x >> 6)] = lower;
-    red[2 * (threadIdx.x >> 6) + 1] = equal;
-  }
-  __syncthreads();
-  lower = equal = 0;
-  for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
-    lower += red[2 * i];
-    equal += red[2 * i + 1];
-  }
-  *first = (int64_t)lower * a.block_m;
-  *last = *first + (int64_t)equal * a.block_m;
-}
+constexpr int kMaxExperts = 512;
 
 // dW[e, n, k] of BM = 16 * MG * WM rows n x BN = 16 * NG * WN columns k, reduced over the expert's slots in
 // steps of 64: the slots' rows of dC (BM columns of each) and of A (BN columns) go through LDS as they lie
-// in memory, kStages steps deep, and both operands are read transposed.  Wave (wm, wn) owns MG 16-row
+// in memory, two steps deep, and both operands are read transposed.  Wave (wm, wn) owns MG 16-row
 // groups of n and NG 16-column tiles of k.
 //
-// The rows are gathered, so a step's loads need its slots' numbers: each wave loads the 64 numbers of a
-// step for itself, by a direct load into its own ring in LDS, early enough that they have landed (by the
-// wait that lets step kt run) when the rows of that step are asked for.  An expert's slots fill its
-// blocks from the front, so only its last step can lack rows; they are zero in both operands.
-template <typename OUT, int MG, int NG, int WM, int WN, int kStages>
+// An expert has few steps (8 at 512 slots), so a workgroup stays for many tiles and asks for the next one's
+// first rows before it stores what it has (32 experts, 11646 slots, N = K = 4096: 553 -> 533 us).  That
+// product needs 283 us of the matrix cores at the rate of a large library product and writes 1.1 GB, 210 us:
+// steps take 2.0 us where the cores need 0.9 to 1.6, and most of the rest is operands that no cache holds
+// yet (with a GB of other data read in front of it the call takes 100 us more).
+//
+// The rows are gathered, so a step's loads need its slots' numbers: these come by direct loads two steps
+// ahead, those of a tile's first two steps while the tile in front of it runs.  An expert's slots fill its
+// blocks from the front, so its steps end with the first that begins with padding, and only the last one
+// can lack rows; they are zero in both operands.
+template <typename OUT, int MG, int NG, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
   constexpr int WAVES = WM * WN, BM = 16 * MG * WM, BN = 16 * NG * WN, ROWS = 64;
   constexpr int PC = BM * 2, PX = BN * 2;                       // bytes of a staged row of dC and of A
   constexpr int CI = ROWS * PC / 1024 / WAVES, XI = ROWS * PX / 1024 / WAVES;  // loads per wave and step
   constexpr int RC = 1024 / PC, RX = 1024 / PX;                 // rows that a load brings
   static_assert(CI * 1024 * WAVES == ROWS * PC && XI * 1024 * WAVES == ROWS * PX, "the waves share the rows evenly");
-  constexpr int CB = ROWS * PC, STAGE = CB + ROWS * PX, LOADS = CI + XI + 1;
-  constexpr int RING = 2 * kStages;                             // steps whose slot numbers are held
-  static_assert(kStages * STAGE >= WAVES * 16 * (32 * NG + 16), "the epilogue's staging fits");
-  __shared__ __attribute__((aligned(128))) uint8_t smem[kStages * STAGE];
-  __shared__ __attribute__((aligned(16))) int s_ids[WAVES][RING][ROWS];
-  __shared__ int red[2 * WAVES];
+  constexpr int CB = ROWS * PC, STAGE = CB + ROWS * PX;
+  constexpr int OWN = MG / WN;                                  // row groups of dbias that a wave sums
+  static_assert(OWN * WN == MG, "the waves share the row groups evenly");
+  __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s_out[WAVES * 16 * (32 * NG + 16)];
+  __shared__ __attribute__((aligned(16))) int s_ids[2][2][ROWS];  // of a tile (in turn) and step (in turn)
+  __shared__ int s_begin[kMaxExperts + 1];                        // blocks of the experts in front of e
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const uint32_t ids_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int*)&s_ids[0][0][0];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const uint32_t ids_lds =
-      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int*)&s_ids[0][0][0] + (uint32_t)w * RING * ROWS * 4;
   const int wm = w / WN, wn = w % WN;
   const int ks = (a.K + BN - 1) / BN, ns = (a.N + BM - 1) / BM;
-  int en, kt0;
-  unit_tile(blockIdx.x, ks, a.group_m, a.group_n, en, kt0);
-  if (kt0 >= ks || en >= ns * a.E) return;
-  const int e = en / ns, nt = en - e * ns;
-  int64_t first, last;
-  expert_range(a, e, red, &first, &last);
-  // the slot numbers of step kt (behind the last entry the last one again)
-  auto issue_ids = [&](int kt) __attribute__((always_inline)) {
-    const int64_t at = min(first + (int64_t)kt * ROWS + lane, last - 1);
-    dma_from<4>(reinterpret_cast<const uint8_t*>(a.sorted + at), ids_lds + (uint32_t)(kt % RING) * ROWS * 4);
-  };
-  int rows = 0;  // the expert's slots
-  if (last > first) {
-#pragma unroll
-    for (int s = 0; s < 2 * (kStages - 1); ++s) issue_ids(s);
-    const int64_t tail = last - a.block_m;
-    rows = (int)(tail - first);
-    for (int i = 0; i < a.block_m; i += 64) {
-      const int s = i + lane < a.block_m ? a.sorted[tail + i + lane] : -1;
-      rows += __popcll(__ballot(s >= 0 && s < a.numel));
-    }
-    rows = __builtin_amdgcn_readfirstlane(rows);
-  }
-  const int KT = (rows + ROWS - 1) / ROWS;
-  const int n0 = nt * BM, k0 = kt0 * BN;
   const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
 
-  int crow[CI], xrow[XI];
-  uint32_t ccol[CI], xcol[XI];  // byte offsets in a row (a column behind the edge reads the first, not stored)
-#pragma unroll
-  for (int l = 0; l < CI; ++l) {
-    crow[l] = (w * CI + l) * RC + lane / (64 / RC);
-    const int place = lane % (64 / RC), col = n0 + ((place >> 1) ^ trans_swizzle(crow[l], PC)) * 16 + (place & 1) * 8;
-    ccol[l] = 2u * (uint32_t)(col < a.N ? col : n0);
+  // The align lists the experts' blocks in rising order, so the counts of their blocks give their ranges.
+  const int nb = min(*a.ntpp / a.block_m, a.cap_blocks);
+  for (int i = tid; i <= a.E; i += 64 * WAVES) s_begin[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < nb; i += 64 * WAVES) {
+    const int e = a.eids[i];
+    if (e >= 0 && e < a.E) atomicAdd(&s_begin[e + 1], 1);
   }
+  __syncthreads();
+  if (w == 0) {
+    int sum = 0;
+    for (int i = 0; i <= a.E; i += 64) {
+      int v = i + lane <= a.E ? s_begin[i + lane] : 0;
 #pragma unroll
-  for (int l = 0; l < XI; ++l) {
-    xrow[l] = (w * XI + l) * RX + lane / (64 / RX);
-    const int place = lane % (64 / RX), col = k0 + ((place >> 1) ^ trans_swizzle(xrow[l], PX)) * 16 + (place & 1) * 8;
-    xcol[l] = 2u * (uint32_t)(col < a.K ? col : k0);
+      for (int d = 1; d < 64; d <<= 1) {
+        const int below = __shfl_up(v, d);
+        v += lane >= d ? below : 0;
+      }
+      v += sum;
+      if (i + lane <= a.E) s_begin[i + lane] = v;
+      sum = __shfl(v, 63);
+    }
   }
-  auto issue = [&](int kt, int stage, int from, int to) __attribute__((always_inline)) {
+  __syncthreads();
+
+  struct Tile {
+    int e, n0, k0, rows;  // rows: entries of the expert, with the padding
+    int64_t first;
+  };
+  auto find = [&](int& at, Tile& t) __attribute__((always_inline)) {  // the first tile from position `at` on
+    for (; at < a.positions; at += gridDim.x) {
+      int en, kt0;
+      unit_tile(at, ks, a.group_m, a.group_n, en, kt0);
+      if (kt0 >= ks || en >= ns * a.E) continue;
+      t.e = en / ns;
+      t.n0 = (en - t.e * ns) * BM;
+      t.k0 = kt0 * BN;
+      const int begin = __builtin_amdgcn_readfirstlane(s_begin[t.e]);
+      t.first = (int64_t)begin * a.block_m;
+      t.rows = (__builtin_amdgcn_readfirstlane(s_begin[t.e + 1]) - begin) * a.block_m;
+      return true;
+    }
+    return false;
+  };
+  // the slot numbers of a tile's step kt (behind the last entry the last one again), loaded by one wave
+  auto issue_ids = [&](const Tile& t, int kt, int turn) __attribute__((always_inline)) {
+    if (t.rows == 0) return;
+    const int64_t at = t.first + min(kt * ROWS + lane, t.rows - 1);
+    dma_from<4>(reinterpret_cast<const uint8_t*>(a.sorted + at), ids_lds + (uint32_t)(turn * 2 + (kt & 1)) * ROWS * 4);
+  };
+  auto exists = [&](const Tile& t, int kt, int turn) __attribute__((always_inline)) {
+    if (kt * ROWS >= t.rows) return false;
+    return (uint32_t)__builtin_amdgcn_readfirstlane(s_ids[turn][kt & 1][0]) < (uint32_t)a.numel;
+  };
+  // byte offsets in a row (a column behind the edge reads the tile's first, not stored)
+  uint32_t ccol[CI], xcol[XI];
+  auto crow = [&](int l) __attribute__((always_inline)) { return (w * CI + l) * RC + lane / (64 / RC); };
+  auto xrow = [&](int l) __attribute__((always_inline)) { return (w * XI + l) * RX + lane / (64 / RX); };
+  auto columns = [&](const Tile& t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int l = 0; l < CI; ++l) {
+      const int place = lane % (64 / RC);
+      const int col = t.n0 + ((place >> 1) ^ trans_swizzle(crow(l), PC)) * 16 + (place & 1) * 8;
+      ccol[l] = 2u * (uint32_t)(col < a.N ? col : t.n0);
+    }
+#pragma unroll
+    for (int l = 0; l < XI; ++l) {
+      const int place = lane % (64 / RX);
+      const int col = t.k0 + ((place >> 1) ^ trans_swizzle(xrow(l), PX)) * 16 + (place & 1) * 8;
+      xcol[l] = 2u * (uint32_t)(col < a.K ? col : t.k0);
+    }
+  };
+  auto issue = [&](const Tile& t, int kt, int turn, int stage, int from, int to) __attribute__((always_inline)) {
     const uint32_t st = smem_lds + (uint32_t)(stage * STAGE);
-    kt = min(kt, KT - 1);
-    const int* ids = s_ids[w][kt % RING];
-    const int left = rows - kt * ROWS;
+    const int* ids = s_ids[turn][kt & 1];
+    const int left = t.rows - kt * ROWS;
 #pragma unroll
     for (int l = 0; l < CI + XI; ++l) {
       if (l < from || l >= to) continue;
-      const int r = l < CI ? crow[l] : xrow[l - CI];
-      const uint32_t s = min((uint32_t)ids[r], (uint32_t)(a.numel - 1));
+      const int r = l < CI ? crow(l) : xrow(l - CI);
+      const uint32_t id = (uint32_t)ids[r];
+      const bool in = r < left && id < (uint32_t)a.numel;
+      const uint32_t s = in ? id : 0u;
       const uint8_t* p;
       if (l < CI) p = reinterpret_cast<const uint8_t*>(a.dC) + (int64_t)s * (a.ld_dc * 2) + ccol[l];
       else p = reinterpret_cast<const uint8_t*>(a.A) + (int64_t)a.row_of(s) * (a.lda * 2) + xcol[l - CI];
-      dma_from<16>(r < left ? p : zero,
+      dma_from<16>(in ? p : zero,
                    st + (l < CI ? (uint32_t)(w * CI + l) * 1024 : CB + (uint32_t)(w * XI + l - CI) * 1024));
     }
   };
 
-  f32x4_t acc[NG][MG];
+  int coff[MG], xoff[NG];
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
+  for (int h = 0; h < MG; ++h) coff[h] = trans_lane(wm * MG + h, PC, lane);
 #pragma unroll
-    for (int h = 0; h < MG; ++h) acc[g][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // dbias is the same reduction with ones in the place of A: the waves of the first tile of columns that
-  // own its first 16 (wn = 0) take it along, two products more for each of the 2 NG.
-  const bool ones = a.dbias && kt0 == 0 && wn == 0;
-  f32x4_t accb[MG];
+  for (int g = 0; g < NG; ++g) xoff[g] = trans_lane(wn * NG + g, PX, lane);
+  auto read_x = [&](const uint8_t* st, int sub, int g) __attribute__((always_inline)) {
+    return trans_operand(st + CB + sub * 32 * PX, xoff[g], PX);
+  };
+  auto read_c = [&](const uint8_t* st, int sub, int h) __attribute__((always_inline)) {
+    return trans_operand(st + sub * 32 * PC, coff[h], PC);
+  };
+
+  int at = blockIdx.x, turn = 0;
+  Tile t;
+  if (!find(at, t)) return;
+  if (w < 2) issue_ids(t, w, 0);
+  wait_vm<0>();
+  block_barrier();
+  bool more = exists(t, 0, 0);
+  columns(t);
+  if (more) issue(t, 0, 0, 0, 0, CI + XI);
+  wait_vm<0>();
+  block_barrier();
+  for (;;) {
+    Tile after;
+    at += gridDim.x;
+    const bool last = !find(at, after);
+    if (!last && w < 2) issue_ids(after, w, turn ^ 1);
+    f32x4_t acc[NG][MG];
 #pragma unroll
-  for (int h = 0; h < MG; ++h) accb[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const u32x4_t one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  if (KT > 0) {
-    int coff[MG], xoff[NG];
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-    for (int h = 0; h < MG; ++h) coff[h] = trans_lane(wm * MG + h, PC, lane);
+      for (int h = 0; h < MG; ++h) acc[g][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // dbias is the same reduction with ones in the place of A: the first tile of columns takes it along, the
+    // WN waves of the same rows MG / WN row groups each.
+    const bool ones = a.dbias && t.k0 == 0;
+    f32x4_t accb[OWN];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) xoff[g] = trans_lane(wn * NG + g, PX, lane);
-    // Step j asks for the rows of step j + kStages - 1 and the numbers of step j + 2 (kStages - 1).
-    wait_vm<0>();
+    for (int i = 0; i < OWN; ++i) accb[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const u32x4_t one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    if (more) {
+      u32x4_t xf[2][NG], cf[2];
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(s, s, 0, CI + XI);
-    wait_vm<(kStages - 2) * (CI + XI)>();
-    block_barrier();
-    u32x4_t xf[2][NG], cf[2];
-    auto read_x = [&](const uint8_t* st, int sub, int g) __attribute__((always_inline)) {
-      return trans_operand(st + CB + sub * 32 * PX, xoff[g], PX);
-    };
-    auto read_c = [&](const uint8_t* st, int sub, int h) __attribute__((always_inline)) {
-      return trans_operand(st + sub * 32 * PC, coff[h], PC);
-    };
+      for (int sub = 0; sub < 2; ++sub) {
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) xf[sub][g] = read_x(smem, sub, g);
-      cf[sub] = read_c(smem, sub, 0);
-    }
-    for (int kt = 0, stage = 0; kt < KT; ++kt) {
-      const uint8_t* st = smem + stage * STAGE;
-      const uint8_t* next = smem + (stage + 1 == kStages ? 0 : stage + 1) * STAGE;
-      const int target = stage == 0 ? kStages - 1 : stage - 1;
-#pragma unroll
-      for (int h = 0; h < MG; ++h) {
-        u32x4_t cn[2];
-        if (h + 1 < MG) {
-          if (h < 2) issue(kt + kStages - 1, target, (CI + XI) * h / 2, (CI + XI) * (h + 1) / 2);
-          if (h == 1) issue_ids(kt + 2 * (kStages - 1));
-          cn[0] = read_c(st, 0, h + 1);
-          cn[1] = read_c(st, 1, h + 1);
-        } else {  // the next step's operands are read behind the last group's products
-          wait_vm<(kStages - 2) * LOADS>();
-          block_barrier();
-          cn[0] = read_c(next, 0, 0);
-          cn[1] = read_c(next, 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            acc[g][h] = mfma(xf[sub][g], cf[sub], acc[g][h]);
-            if (h + 1 == MG) xf[sub][g] = read_x(next, sub, g);
-          }
-        if (ones) {
-          accb[h] = mfma(one, cf[0], accb[h]);
-          accb[h] = mfma(one, cf[1], accb[h]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        cf[0] = cn[0];
-        cf[1] = cn[1];
+        for (int g = 0; g < NG; ++g) xf[sub][g] = read_x(smem, sub, g);
+        cf[sub] = read_c(smem, sub, 0);
       }
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      for (int kt = 0; more; ++kt) {
+        const uint8_t* st = smem + (kt & 1) * STAGE;
+        const uint8_t* next = smem + (~kt & 1) * STAGE;
+        more = exists(t, kt + 1, turn);
+#pragma unroll
+        for (int h = 0; h < MG; ++h) {
+          u32x4_t cn[2];
+          if (h + 1 < MG) {
+            if (h < 2 && more)
+              issue(t, kt + 1, turn, ~kt & 1, (CI + XI) * h / 2, (CI + XI) * (h + 1) / 2);
+            if (h == 1 && more && w == 0) issue_ids(t, kt + 2, turn);
+            cn[0] = read_c(st, 0, h + 1);
+            cn[1] = read_c(st, 1, h + 1);
+          } else {  // the next step's operands are read behind the last group's products (not used after the last step)
+            wait_vm<0>();
+            block_barrier();
+            cn[0] = read_c(next, 0, 0);
+            cn[1] = read_c(next, 1, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              acc[g][h] = mfma(xf[sub][g], cf[sub], acc[g][h]);
+              if (h + 1 == MG) xf[sub][g] = read_x(next, sub, g);
+            }
+          if (ones && h / OWN == wn) {
+            accb[h % OWN] = mfma(one, cf[0], accb[h % OWN]);
+            accb[h % OWN] = mfma(one, cf[1], accb[h % OWN]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          cf[0] = cn[0];
+          cf[1] = cn[1];
+        }
+      }
+    } else {
+      wait_vm<0>();
+      block_barrier();
     }
+    // Every wave has passed the last step's barrier: its stage is free, and the other holds nothing.
+    if (!last) {
+      more = exists(after, 0, turn ^ 1);
+      columns(after);
+      if (more) issue(after, 0, turn ^ 1, 0, 0, CI + XI);
+    }
+    if (ones && lane < 16) {  // (every row of the product is the sum; lane l < 16 holds row 0 of column l)
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        const int n = t.n0 + (wm * MG + wn * OWN + i) * 16 + lane;
+        if (n >= a.N) continue;
+        const int64_t to = (int64_t)t.e * a.N + n;
+        if constexpr (sizeof(OUT) == 4) static_cast<float*>(a.dbias)[to] = accb[i][0];
+        else static_cast<uint16_t*>(a.dbias)[to] = f32_to_bf16(accb[i][0]);
+      }
+    }
+    store_tiles<NG, MG, OUT>(acc, MG, s_out, w, lane, t.k0 + wn * 16 * NG, a.K, true, [&](int r) -> OUT* {
+      const int n = t.n0 + wm * 16 * MG + r;
+      return n < a.N ? static_cast<OUT*>(a.dW) + ((int64_t)t.e * a.N + n) * a.K : nullptr;
+    });
+    if (last) break;
     wait_vm<0>();
     block_barrier();
+    t = after;
+    turn ^= 1;
   }
-  if (ones && lane < 16) {  // (every row of the product is the sum; lane l < 16 holds row 0 of column l)
-#pragma unroll
-    for (int h = 0; h < MG; ++h) {
-      const int n = n0 + (wm * MG + h) * 16 + lane;
-      if (n >= a.N) continue;
-      const int64_t at = (int64_t)e * a.N + n;
-      if constexpr (sizeof(OUT) == 4) static_cast<float*>(a.dbias)[at] = accb[h][0];
-      else static_cast<uint16_t*>(a.dbias)[at] = f32_to_bf16(accb[h][0]);
-    }
-  }
-  store_tiles<NG, MG, OUT>(acc, MG, smem, w, lane, k0 + wn * 16 * NG, a.K, true, [&](int r) -> OUT* {
-    const int n = n0 + wm * 16 * MG + r;
-    return n < a.N ? static_cast<OUT*>(a.dW) + ((int64_t)e * a.N + n) * a.K : nullptr;
-  });
 }
 
 // dst[r, :] = sum over the live slots of row r, in slot order (fp32, one rounding), of src[slot, :]
@@ -256,17 +293,15 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
   }
 }
 
-template <typename OUT, int MG, int NG, int WM, int WN, int kStages>
-static int launch_wgrad_tile(const char* fn, GradArgs a, hipStream_t st) {
+template <typename OUT, int MG, int NG, int WM, int WN>
+static int launch_wgrad_tile(const char* fn, GradArgs a, int per_cu, hipStream_t st) {
   constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
   const int64_t tiles = (int64_t)((a.N + BM - 1) / BM) * a.E, strips = (a.K + BN - 1) / BN;
-  const int64_t unit = std::min<int64_t>(32, std::max<int64_t>(1, tiles * strips / kXcds));
-  a.group_m = (int32_t)std::min<int64_t>({4, tiles, unit});
-  a.group_n = (int32_t)std::min<int64_t>(strips, std::max<int64_t>(1, unit / a.group_m));
-  const int64_t units = (tiles + a.group_m - 1) / a.group_m * ((strips + a.group_n - 1) / a.group_n);
-  const int64_t grid = (units + kXcds - 1) / kXcds * kXcds * a.group_m * a.group_n;
-  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
-  hipLaunchKernelGGL((wgrad_kernel<OUT, MG, NG, WM, WN, kStages>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, st, a);
+  const int64_t positions = choose_units(tiles, strips, &a.group_m, &a.group_n);
+  MOE_REQUIRE(positions < (1ll << 30), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+  a.positions = (int32_t)positions;
+  const int64_t grid = std::min<int64_t>(positions, (device_cu_count() * per_cu + kXcds - 1) / kXcds * kXcds);
+  hipLaunchKernelGGL((wgrad_kernel<OUT, MG, NG, WM, WN>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, st, a);
   return check_launch(fn);
 }
 
@@ -275,8 +310,8 @@ static int launch_wgrad_tile(const char* fn, GradArgs a, hipStream_t st) {
 template <typename OUT>
 static int launch_wgrad(const char* fn, const GradArgs& a, hipStream_t st) {
   if ((int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E >= device_cu_count())
-    return launch_wgrad_tile<OUT, 8, 4, 2, 4, 2>(fn, a, st);
-  return launch_wgrad_tile<OUT, 4, 2, 2, 4, 2>(fn, a, st);
+    return launch_wgrad_tile<OUT, 8, 4, 2, 4>(fn, a, 1, st);
+  return launch_wgrad_tile<OUT, 4, 2, 2, 4>(fn, a, 2, st);
 }
 
 static int check_grad(const char* fn, const void* dC, int64_t ld_dc, int32_t E, int32_t N, int32_t K, int64_t numel,
@@ -353,7 +388,7 @@ extern "C" int moe_bf16_gemm_wgrad(const uint16_t* dC, int64_t ld_dc, const uint
   rc = moe_align_capacity(numel, 1, E, block_m, &cap, &cap_blocks);
   if (rc) return rc;
   GradArgs a{dC, ld_dc, A, lda, dW, dbias, sorted_token_ids, expert_ids, num_tokens_post_padded, (int32_t)numel, top_k,
-             block_m, N, K, E, (int32_t)cap_blocks, 0, 0, 0, 0};
+             block_m, N, K, E, (int32_t)cap_blocks, 0, 0, 0, 0, 0};
   if (top_k > 1) {  // ceil(2^(32 + shift) / top_k): exact for numerators below 2^31
     while ((2u << a.div_shift) < (uint32_t)top_k) ++a.div_shift;
     a.div_mul = (uint32_t)(((1ull << (32 + a.div_shift)) + top_k - 1) / (uint64_t)top_k);

@@ -274,7 +274,9 @@ static int launch_stream(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hi
 // first lg are live.  acc[g][h] holds, in lane l, columns 4 (l / 16) + 0..3 of tile g of row l % 16
 // of group h.  bf16 rows go through the wave's own part of LDS (idle: every wave has passed the last
 // step's barrier), so that a store instruction covers whole segments of 32 * NG bytes of a row with
-// 16 bytes a lane.  row_ptr(r) is where row r starts, or null.
+// 16 bytes a lane.  row_ptr(r) is where row r starts, or null.  The stores pass the L2 by: what a tile
+// writes would push the operands that the XCD's workgroups share out of it (weight gradients of 32 experts,
+// N = K = 4096: 588 -> 508 us; Zipf prefill of 4096 tokens 914 -> 887, of 1024 in bf16 600 -> 584).
 template <int NG, int MG, typename OUT, typename RowPtr>
 __device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg, uint8_t* smem, int w, int lane,
                                             int n0, int N, bool wide, RowPtr row_ptr) {
@@ -286,7 +288,7 @@ __device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const int n = n0 + g * 16 + 4 * (lane >> 4);
-        if (row && n < N) *reinterpret_cast<f32x4_t*>(row + n) = acc[g][h];
+        if (row && n < N) __builtin_nontemporal_store(acc[g][h], reinterpret_cast<f32x4_t*>(row + n));
       }
     }
   } else {
@@ -325,7 +327,7 @@ __device__ __forceinline__ void store_tiles(const f32x4_t (&acc)[NG][MG], int lg
         if (RPI > 16 && r >= 16) continue;  // (one tile: 32 rows' worth of lanes, 16 rows)
         OUT* row = row_ptr(h * 16 + r);
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(wl + r * PITCH + 16 * j);
-        if (row && n0 + 8 * j < N) *reinterpret_cast<u32x4_t*>(row + n0 + 8 * j) = v;
+        if (row && n0 + 8 * j < N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(row + n0 + 8 * j));
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -394,6 +396,29 @@ __host__ __device__ inline void unit_tile(int P, int strips, int group_m, int gr
   const int j = P / kXcds, u = j / U * kXcds + P % kXcds, r = j % U;
   mb = u / across * group_m + r % group_m;
   strip = u % across * group_n + r / group_m;
+}
+
+// The units for `tiles` x `strips` workgroups, and the launch's size.  4 x 8, a workgroup for each CU of an
+// XCD, or smaller ones where eight XCDs would share these unevenly: the first shape whose fullest XCD has
+// within a sixteenth of the least.  Strips are split evenly.
+// (Measured on the Zipf prefill product: units of 1 x all strips, 2 x 16 and 4 x 8 1076, 1024, 999 us.
+// 4608 slots on 8 experts, 26 x 8 workgroups: in units of 4 x 6, hence 4 x 2 at the edge, which go to every
+// other XCD, K = 512 and 2048 take 36 and 91 us, in units of 4 x 4 21 and 51.)
+static int64_t choose_units(int64_t tiles, int64_t strips, int32_t* group_m, int32_t* group_n) {
+  int64_t gm[6], gn[6], load[6], best = INT64_MAX;
+  for (int i = 0; i < 6; ++i) {
+    gm[i] = std::min<int64_t>(tiles, 4 >> (i / 2));
+    const int64_t across = (strips + 7) / 8 << (i % 2);
+    gn[i] = (strips + across - 1) / across;
+    const int64_t units = ((tiles + gm[i] - 1) / gm[i]) * ((strips + gn[i] - 1) / gn[i]);
+    load[i] = (units + kXcds - 1) / kXcds * gm[i] * gn[i];
+    best = std::min(best, load[i]);
+  }
+  int i = 0;
+  while (load[i] > best + best / 16) ++i;
+  *group_m = (int32_t)gm[i];
+  *group_n = (int32_t)gn[i];
+  return load[i] * kXcds;
 }
 
 // A tile of BM entries made of several blocks: an expert's blocks follow each other, and the ones whose
@@ -760,15 +785,8 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
     const int64_t per = BM / a.block_m, experts = std::min<int64_t>(a.E, a.numel);
     tiles = std::min(cap_blocks, (cap_blocks + experts * (per - 1)) / per);
   }
-  // Units of 4 x 8, a workgroup for each CU of an XCD, or smaller ones where there are not eight of them.
-  // (Measured on the Zipf prefill product: units of 1 x all strips, 2 x 16 and 4 x 8 1076, 1024, 999 us;
-  // units that take all strips leave some XCDs a quarter of the tiles more than others.)
-  const int64_t strips = (a.N + BN - 1) / BN, unit = std::min<int64_t>(32, std::max<int64_t>(1, tiles * strips / kXcds));
-  a.group_m = (int32_t)std::min<int64_t>({4, tiles, unit});
-  a.group_n = (int32_t)std::min<int64_t>(strips, std::max<int64_t>(1, unit / a.group_m));
+  const int64_t grid = choose_units(tiles, (a.N + BN - 1) / BN, &a.group_m, &a.group_n);
   a.tiles = (int32_t)tiles;
-  const int64_t units = (tiles + a.group_m - 1) / a.group_m * ((strips + a.group_n - 1) / a.group_n);
-  const int64_t grid = (units + kXcds - 1) / kXcds * kXcds * a.group_m * a.group_n;
   MOE_REQUIRE(grid < (1ll << 31) && tiles < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
   hipLaunchKernelGGL((block_gemm_tile_kernel<T, MG, NG, WM, WN, kStages, kMerge>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, a);
