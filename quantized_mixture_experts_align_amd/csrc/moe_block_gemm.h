@@ -795,14 +795,18 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
 
 // The kernel for a call.  Blocks of at most 16 rows stream their weights (block_gemm_stream_kernel).  For
 // the others the tile shape with the least rounds of resident workgroups (half way between the whole
-// number and the fraction: later ones start as earlier ones end) x time of one, for KT steps of 128 bytes of K (fitted to dense e4m3fn products of 8 to 56 steps; bf16's have the same proportions):
+// number and the fraction: later ones start as earlier ones end) x time of one, for KT steps of 128 bytes
+// of K (fitted to dense e4m3fn products of 8 to 56 steps; bf16's have the same proportions):
 //   256 x 256, one a CU    10.4 + 1.68 KT us        128 x 128, two a CU   5.7 + 1.18 KT us
 //   128 x 256, one a CU     6.4 + 1.07 KT us         64 x 64, two a CU    2.8 + 0.51 KT us
-//    64 x 256, one a CU     3.6 + 0.70 KT us
-// and 4 us more for finding the tile's expert and rows.  The rows of routed experts are taken as spread
-// evenly, each expert ending half way through a tile.  256-row tiles are made of an expert's 128-row
-// blocks, counted in the kernel (2 us more), where the batch has 128 slots an expert (1024 Zipf tokens of 8
-// choices on 32 of 256 experts: 618 us with 128 rows, 604 with 256; 4096 of them 975 and 908).
+//    64 x 256, one a CU     3.6 + 0.90 KT us
+// and 4 us more for finding the tile's expert and rows.  (Dense products fit 0.70 KT for 64 x 256; 0.90 picks
+// better among routed ones.)  The rows of routed experts are taken as spread evenly, each expert ending
+// half way through a tile.  Over 253 drawn calls of all three products the shape chosen takes 4 % more than
+// the best of the five on average, 14 % at nine in ten: experts' sizes are not known here.  256-row tiles are
+// made of an expert's 128-row blocks, counted in the kernel (2 us more), where the batch has 128 slots an
+// expert (1024 Zipf tokens of 8 choices on 32 of 256 experts: 618 us with 128 rows, 604 with 256; 4096 of
+// them 975 and 908).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
   if constexpr (!T::kTrans) {
@@ -832,7 +836,7 @@ static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap
     const double whole = (double)((n + cus * per_cu - 1) / (cus * per_cu));
     return (exact + whole) / 2 * (fixed + (a.sorted ? 4.0 : 0.0) + step * (double)KT);
   };
-  const double small = cost(64, 64, 2, 2.8, 0.51), flat = cost(64, 256, 1, 3.6, 0.70);
+  const double small = cost(64, 64, 2, 2.8, 0.51), flat = cost(64, 256, 1, 3.6, 0.90);
   if (a.block_m <= 32) {  // (at most 32 rows: the 64-row tiles' shapes with half the rows)
     if (small < flat) return launch_tile<T, 2, 1, 1, 4, 4>(fn, a, cap_blocks, st);
     return launch_tile<T, 2, 4, 1, 4, 2>(fn, a, cap_blocks, st);
