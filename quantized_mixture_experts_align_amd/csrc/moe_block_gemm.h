@@ -138,6 +138,7 @@ __device__ __forceinline__ void gemm_stream(const BlockGemmArgs& a, f32x4_t (&pa
   const int strip = blockIdx.x % strips, b = blockIdx.x / strips;
   int e = 0, blocks = 1;
   if (a.sorted) {
+    const int nb = *a.ntpp / a.block_m;
     e = a.eids[b];
     if constexpr (MB == 2) {
       // the expert's blocks in front of b, and whether the next one is its too
@@ -153,9 +154,9 @@ __device__ __forceinline__ void gemm_stream(const BlockGemmArgs& a, f32x4_t (&pa
         before += 64;
       }
       if (before & 1) return;  // (the block in front takes this one along)
-      blocks = next == e ? 2 : 1;
+      blocks = next == e && b + 1 < nb ? 2 : 1;
     }
-    if ((int64_t)b * a.block_m >= *a.ntpp || e < 0 || e >= a.E) return;
+    if (b >= nb || e < 0 || e >= a.E) return;
   }
   const int KT = (a.Kb + kStepBytes - 1) / kStepBytes;
   const int kt0 = KT * w / KS, kt1 = KT * (w + 1) / KS;
