@@ -22,23 +22,26 @@ def skewed(M, k, E, seed):
     return r.choice(E, size=(M, k), p=p / p.sum()).astype(np.int32)
 
 
-# (M, k, E, N, K of bf16 values, B): sizes for which the launch takes, in turn, streamed blocks in pairs (odd
-# and even counts of them, short blocks), 64 x 256 tiles of blocks of 32 and of 64, 128 x 128, 128 x 256,
-# 256 x 256 of one block and of several, and more blocks than a wave looks through at once
-TILES = [(200, 2, 8, 520, 72, 16), (120, 4, 8, 392, 136, 5), (400, 2, 8, 4096, 264, 32), (400, 2, 8, 4096, 264, 64),
-         (1792, 2, 4, 2048, 256, 128), (1792, 2, 4, 2048, 1024, 128), (1500, 1, 3, 4104, 136, 256),
-         (9000, 1, 3, 1032, 72, 128), (15000, 1, 3, 264, 72, 128)]
+# (M, k, E, N, K of bf16 values, B): sizes for which the launch takes, in turn, streamed blocks one by one with
+# K over eight waves and over four, in pairs (odd and even counts of them, short blocks), 64 x 256 tiles of
+# blocks of 32 and of 64, 128 x 128, 128 x 256, 256 x 256 of one block and of several (more blocks than a wave
+# looks through at once), and tiles of an expert's last block
+TILES = [(4, 2, 4, 264, 1544, 16), (16, 2, 16, 1032, 136, 16), (200, 2, 8, 520, 72, 16), (120, 4, 8, 392, 136, 5),
+         (400, 2, 8, 4096, 264, 32), (400, 2, 8, 4096, 264, 64), (1792, 2, 4, 2048, 256, 128),
+         (1792, 2, 4, 2048, 1024, 128), (1500, 2, 3, 4104, 136, 256), (5500, 2, 3, 1032, 136, 128),
+         (15000, 1, 3, 264, 72, 128)]
 
 
 @pytest.mark.parametrize("M,k,E,N,K,B", TILES)
 @pytest.mark.parametrize("top", [1, 0])
 def test_bf16_product_and_rows_gradient(M, k, E, N, K, B, top):
-    """top: A has a row for each slot (1) or for each token (0); the output's rows are 8-byte aligned."""
+    """top: A has a row for each slot (1) or for each token (0); the output's rows are 8-byte aligned; slots of
+    expert E are dropped."""
     top_k = top or k
-    al, local = aligned(skewed(M, k, E, M), 0, E, B)
+    al, local = aligned(skewed(M, k, E + 1, M), 0, E, B)
     a, w, b = bf16((M * k // top_k, K), M), bf16((E, N, K), N), bf16((E, N), K)
     W, base = w.cuda(), torch.full((M * k, N + 4), -5.0, dtype=torch.bfloat16, device="cuda")
-    P.moe_bf16_gemm(a.cuda(), W, *al[:3], M * k, top_k, B, bias=b.cuda(), out=base[:, :N])
+    P.moe_bf16_gemm(a.cuda(), W, *al[:3], M * k, top_k, B, bias=b.cuda(), out=base[:, :N], slot_local_ids=al[3])
     A64, W64 = a.double().numpy(), w.double().numpy()
     want, bound = product(A64, W64, b.double().numpy(), local, top_k)
     assert_close(base[:, :N], want, bound + U16 * np.abs(want) + 1e-30, "C")
@@ -64,6 +67,14 @@ def test_w8a8_product(M, k, E, N, K, B):
     want, bound = product8(a, sa, w, sb, None, local, k)
     assert_close(base[:, :N], want, bound + U16 * np.abs(want) + 1e-30, "C")
     assert bool((base[:, N:] == -5.0).all())
+
+
+def test_linear_of_256_row_tiles():
+    M, N, K = 3000, 4104, 272
+    a, sa, w, sb = e4m3((M, K), 1), scales((M, 3), 1), e4m3((1, N, K), 2), scales((1, 33, 3), 2)
+    got = P.moe_w8a8_linear(a.cuda(), sa.cuda(), w[0].cuda(), sb[0].cuda())
+    want, bound = product8(a, sa, w, sb, None, np.zeros(M, np.int32), 1)
+    assert_close(got, want, bound + U16 * np.abs(want) + 1e-30, "C")
 
 
 # 256 x 256 tiles and 128 x 128 ones, of which a workgroup computes several; experts of no, one and many steps
