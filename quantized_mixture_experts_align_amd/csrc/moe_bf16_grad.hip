@@ -42,9 +42,9 @@ constexpr int kMaxExperts = 512;
 //
 // An expert has few steps (8 at 512 slots), so a workgroup stays for many tiles and asks for the next one's
 // first rows before it stores what it has (32 experts, 11646 slots, N = K = 4096: 553 -> 533 us).  That
-// product needs 283 us of the matrix cores at the rate of a large library product and writes 1.1 GB, 210 us:
-// steps take 2.0 us where the cores need 0.9 to 1.6, and most of the rest is operands that no cache holds
-// yet (with a GB of other data read in front of it the call takes 100 us more).
+// product needs 283 us of the matrix cores at the rate of a large library product and writes 1.1 GB, 210 us.
+// Of a tile's 17 us on average 6.2 steps take 12.8, the stores 2.9, the rest 1.4; where no cache holds the
+// operands yet (a GB of other data read in front) steps and stores take 14.5 and 4.3.
 //
 // The rows are gathered, so a step's loads need its slots' numbers: these come by direct loads two steps
 // ahead, those of a tile's first two steps while the tile in front of it runs.  An expert's slots fill its
@@ -305,8 +305,9 @@ static int launch_wgrad_tile(const char* fn, GradArgs a, int per_cu, hipStream_t
   return check_launch(fn);
 }
 
-// 256 x 256 tiles (8192 slots on 8 experts, N = K = 4096: 317 us; 128 x 256 417, 128 x 128 405), or 128 x 128
-// where these leave CUs without work (4608 slots on 8 experts, N = 2048, K = 512: 28.5 and 20.9 us).
+// 256 x 256 tiles, or 128 x 128 where these leave CUs without work (8192 slots on 8 experts, N = K = 4096: 303
+// and 382 us; 4608 slots on 8 experts, N = 2048: K = 1024, 256 of the larger tiles, 29 and 36 us, K = 512, 128 of
+// them, 27 and 20 us).
 template <typename OUT>
 static int launch_wgrad(const char* fn, const GradArgs& a, hipStream_t st) {
   if ((int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E >= device_cu_count())

@@ -11,6 +11,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
+
 GROUP = 128           # columns that share an activation scale, rows and columns of a weight block
 _F8 = (torch.float8_e4m3fn, torch.uint8)
 
@@ -329,7 +330,11 @@ def moe_experts_linear(A: torch.Tensor, W: torch.Tensor, align, top_k: int, bloc
     num_tokens_post_padded, slot_local_ids) with the same block_m; A has numel // top_k rows (one
     for each token with the layer's top_k, or one for each slot with top_k = 1).  Gradients flow to
     A, W and bias; they are bf16, once differentiable, and zero for rows and experts without slots.
-    expected_slots as moe_w8a8_gemm."""
+    expected_slots as moe_w8a8_gemm.
+
+    The forward and the backward pass can be captured into a graph.  As with any autograd work, hold no
+    graph of an eager call of the same leaves while capturing: torch then waits on the eager call's
+    stream inside the capture, which ends the process."""
     sorted_ids, expert_ids, ntpp, slot_local = align
     if slot_local is None:
         raise ValueError("moe_experts_linear needs the align's slot_local_ids")
