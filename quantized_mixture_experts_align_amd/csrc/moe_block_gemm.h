@@ -128,8 +128,8 @@ __device__ __forceinline__ void zero_dropped(const BlockGemmArgs& a, int mine) {
 // ---------------------------------------------------------------------------- few rows
 // Workgroup = up to 16 slots of a block (MB = 2: of two consecutive blocks of one expert) x NG 16-row
 // weight tiles, K split over its KS waves, operands straight from memory to registers in chunks of
-// kChunk steps, partial sums joined through LDS in wave order.  The cost is the stream of weights (64 tokens of 8 choices on 32 of 256
-// experts, N = 8192, K = 4096: 139 us, 6.7 TB/s).
+// kChunk steps, partial sums joined through LDS in wave order.  The cost is the stream of weights (64 tokens
+// of 8 choices on 32 of 256 experts, N = 8192, K = 4096: 142 us, 6.6 TB/s).
 template <typename T, int NG, int KS, int MB>
 __device__ __forceinline__ void gemm_stream(const BlockGemmArgs& a, f32x4_t (&part)[KS][NG * MB][64]) {
   constexpr int kChunk = 4;
@@ -470,6 +470,7 @@ template <typename T, int MG, int NG, int WM, int WN, int kStages>
 struct TileShape {
   static constexpr int WAVES = WM * WN, BM = 16 * MG * WM, BN = 16 * NG * WN;
   static constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;   // direct loads per wave and step, 1 KB each
+  static_assert(MG >= 2, "a step's loads are asked for in its row groups but the last");
   static_assert(XI * 8 * WAVES == BM && WI * 8 * WAVES == BN, "the waves share the staged rows evenly");
   static constexpr int SR = BM / WAVES, SP = SR + 4;  // rows whose scales a wave loads; its place for them
   static constexpr int XB = BM * kStepBytes, WB = BN * kStepBytes;
@@ -481,7 +482,7 @@ struct TileShape {
 template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge>
 constexpr int tile_bytes() {
   constexpr int full = TileShape<T, MG, NG, WM, WN, kStages>::BYTES;
-  if constexpr (kMerge) {
+  if constexpr (kMerge && MG >= 4) {
     constexpr int half = TileShape<T, MG / 2, NG, WM, WN, kStages + 1>::BYTES;
     return half > full ? half : full;
   }
@@ -738,9 +739,9 @@ __device__ __forceinline__ void gemm_tile(const BlockGemmArgs& a, uint8_t* smem,
 // and the first steps' operands before the tile's rows are counted.  (two waves a SIMD: one workgroup of
 // eight waves a CU, or two of four.)
 //
-// With kMerge a tile of BM rows is made of several blocks of an expert, and an expert's last tile that
-// holds no more than half of them runs in the shape of half the rows with a stage more: a step of a half
-// filled tile costs nearly what a full one's does.
+// With kMerge a tile of BM rows is made of several blocks of an expert, and an expert's last tile of 64 rows
+// and more that holds no more than half of them runs in the shape of half the rows with a stage more: a step
+// of a half filled tile costs nearly what a full one's does.
 template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge>
 __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockGemmArgs a) {
   constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
@@ -759,8 +760,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
       const int rows = merged_tile(a, nb, BM, mb, &b, &e);
       if (rows == 0) return;
       const int64_t first = (int64_t)b * a.block_m;
-      if (rows > BM / 2) gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, first, rows, e, strip);
-      else gemm_tile<T, MG / 2, NG, WM, WN, kStages + 1>(a, smem, s_slot, first, rows, e, strip);
+      if constexpr (MG >= 4) {
+        if (rows <= BM / 2) return gemm_tile<T, MG / 2, NG, WM, WN, kStages + 1>(a, smem, s_slot, first, rows, e, strip);
+      }
+      gemm_tile<T, MG, NG, WM, WN, kStages>(a, smem, s_slot, first, rows, e, strip);
     } else {
       const int b = mb / subs, sub = mb - b * subs;
       int e = 0;
@@ -777,15 +780,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_gemm_tile_kernel(BlockG
   if constexpr (!T::kScaled) zero_dropped<typename T::Out>(a, flags);
 }
 
+// Most tiles of BM rows that the blocks can make (an expert's last tile may hold fewer blocks).
+static int64_t merged_tiles(const BlockGemmArgs& a, int64_t cap_blocks, int BM) {
+  const int64_t per = BM / a.block_m, experts = std::min<int64_t>(a.E, a.numel);
+  return std::min(cap_blocks, (cap_blocks + experts * (per - 1)) / per);
+}
+
 template <typename T, int MG, int NG, int WM, int WN, int kStages, bool kMerge = false>
 static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipStream_t st) {
   constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
   a.cap_blocks = (int32_t)cap_blocks;
-  int64_t tiles = cap_blocks * ((a.block_m + BM - 1) / BM);
-  if (kMerge) {  // an expert's last tile may hold fewer blocks
-    const int64_t per = BM / a.block_m, experts = std::min<int64_t>(a.E, a.numel);
-    tiles = std::min(cap_blocks, (cap_blocks + experts * (per - 1)) / per);
-  }
+  const int64_t tiles = kMerge ? merged_tiles(a, cap_blocks, BM) : cap_blocks * ((a.block_m + BM - 1) / BM);
   const int64_t grid = choose_units(tiles, (a.N + BN - 1) / BN, &a.group_m, &a.group_n);
   a.tiles = (int32_t)tiles;
   MOE_REQUIRE(grid < (1ll << 31) && tiles < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
@@ -810,23 +815,34 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
 // them 975 and 908).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
+  const int64_t cus = device_cu_count(), KT = (a.Kb + kStepBytes - 1) / kStepBytes;
+  constexpr int64_t kMaxMerged = 4096;  // blocks that every workgroup counts through, 64 at a time
+  // 16-row blocks from 12 slots an expert, when experts have more than one often enough, and enough experts for
+  // every CU: two blocks in a 32-row tile, weights through LDS as whole cache lines.  With most rows live the
+  // streamed form's loads, 16 rows an instruction, are what takes the time, unless K is long (16 slots each on
+  // 128 experts, N = K = 2880: 245 and 221 us; on 64, N = 1024, K = 2048: 35 and 24; on 32, N = 8192, K = 4096: 209
+  // and 223 us, and with 2 live slots each where 16 were expected 149 and 206).  The rows gradient takes 365 us
+  // for the first of these, in blocks one by one 405.
+  if (a.block_m == 16 && a.sorted && cap_blocks <= kMaxMerged && a.expected >= 12ll * a.E &&
+      (int64_t)a.E * ((a.N + 127) / 128) >= cus && (T::kTrans || KT < 28))
+    return launch_tile<T, 2, 2, 1, 4, 3, true>(fn, a, cap_blocks, st);
   if constexpr (!T::kTrans) {
     if (a.block_m <= 16) {
-      // Two tiles and four waves a workgroup, or one tile where that leaves CUs with one workgroup or none,
-      // with eight waves along a long K (a dense row, N = 4096: K = 7168 15.6, 12.1, 8.4 us for the three;
-      // K = 512 3.8, 3.4, 5.0 us).  Four tiles and two blocks of an expert together where experts have more
-      // rows than one block holds often enough (16 slots each on 128 experts, N = K = 2880: 302 -> 245 us;
-      // with 2 slots each on 32 experts nothing is gained, 139 and 140 us).
-      const int64_t cus = device_cu_count();
+      // One tile a workgroup where two would leave CUs without one, with eight waves along a long K (a dense row,
+      // N = 4096: K = 7168 two tiles and four waves 11.3, one and four 11.4, one and eight 9.7 us; K = 512 3.8,
+      // 3.4, 5.0 us), and for bf16 rows of 6 KB and more while experts have one block (20 slots on 8 experts,
+      // N = K = 4096: 52, 56, 44 us; e4m3 ones of 7 KB, 32 slots on 32 experts, 115 and 129 us for the first and
+      // the last).  Else two tiles and four waves, and from four slots an expert four tiles, which read the rows of
+      // A half as often, and two blocks of an expert together where it has them (K = 4096, N = 8192, 32 experts,
+      // 2, 4, 8 slots each: 162, 181, 197 and 163, 182, 189 us; Zipf, 8 slots: 211 and 188 us).
       const int64_t n = (int64_t)((a.N + 31) / 32) * (a.sorted ? std::min<int64_t>(cap_blocks, a.expected) : cap_blocks);
-      if (n < cus && a.Kb >= 24 * kStepBytes) return launch_stream<T, 1, 8, 1>(fn, a, cap_blocks, st);
-      if (n < 2 * cus) return launch_stream<T, 1, 4, 1>(fn, a, cap_blocks, st);
-      if (a.sorted && a.expected >= 10ll * a.E) return launch_stream<T, 4, 4, 2>(fn, a, cap_blocks, st);
+      if (n < cus ? KT >= 24 : !T::kScaled && KT >= 48 && a.expected < 12ll * a.E)
+        return launch_stream<T, 1, 8, 1>(fn, a, cap_blocks, st);
+      if (n < cus) return launch_stream<T, 1, 4, 1>(fn, a, cap_blocks, st);
+      if (a.sorted && a.expected >= 4ll * a.E) return launch_stream<T, 4, 4, 2>(fn, a, cap_blocks, st);
       return launch_stream<T, 2, 4, 1>(fn, a, cap_blocks, st);
     }
   }
-  const int64_t cus = device_cu_count(), KT = (a.Kb + kStepBytes - 1) / kStepBytes;
-  constexpr int64_t kMaxMerged = 4096;  // blocks that every workgroup counts through, 64 at a time
   const bool merge = a.sorted && a.block_m == 128 && cap_blocks <= kMaxMerged && a.expected >= 128ll * a.E;
   auto cost = [&](int BM, int BN, int per_cu, double fixed, double step) {
     const int64_t tiles = a.sorted ? std::min(cap_blocks * ((a.block_m + BM - 1) / BM),

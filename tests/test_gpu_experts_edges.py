@@ -23,13 +23,14 @@ def skewed(M, k, E, seed):
 
 
 # (M, k, E, N, K of bf16 values, B): sizes for which the launch takes, in turn, streamed blocks one by one with
-# K over eight waves and over four, in pairs (odd and even counts of them, short blocks), 64 x 256 tiles of
-# blocks of 32 and of 64, 128 x 128, 128 x 256, 256 x 256 of one block and of several (more blocks than a wave
-# looks through at once), and tiles of an expert's last block
-TILES = [(4, 2, 4, 264, 1544, 16), (16, 2, 16, 1032, 136, 16), (200, 2, 8, 520, 72, 16), (120, 4, 8, 392, 136, 5),
-         (400, 2, 8, 4096, 264, 32), (400, 2, 8, 4096, 264, 64), (1792, 2, 4, 2048, 256, 128),
-         (1792, 2, 4, 2048, 1024, 128), (1500, 2, 3, 4104, 136, 256), (5500, 2, 3, 1032, 136, 128),
-         (15000, 1, 3, 264, 72, 128)]
+# K over eight waves (few of them; long rows of bf16) and over four, in pairs (odd and even counts of them, short
+# blocks), 16-row blocks in 32-row tiles, 64 x 256 tiles of blocks of 32 and of 64, 128 x 128, 128 x 256,
+# 256 x 256 of one block and of several (more blocks than a wave looks through at once), and tiles of an
+# expert's last block
+TILES = [(4, 2, 4, 264, 1544, 16), (8, 2, 8, 1032, 3112, 16), (16, 2, 16, 1032, 136, 16), (200, 2, 8, 520, 72, 16),
+         (120, 4, 8, 392, 136, 5), (450, 2, 64, 520, 136, 16), (400, 2, 8, 4096, 264, 32), (400, 2, 8, 4096, 264, 64),
+         (1792, 2, 4, 2048, 256, 128), (1792, 2, 4, 2048, 1024, 128), (1500, 2, 3, 4104, 136, 256),
+         (5500, 2, 3, 1032, 136, 128), (15000, 1, 3, 264, 72, 128)]
 
 
 @pytest.mark.parametrize("M,k,E,N,K,B", TILES)
