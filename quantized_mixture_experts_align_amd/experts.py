@@ -332,9 +332,10 @@ def moe_experts_linear(A: torch.Tensor, W: torch.Tensor, align, top_k: int, bloc
     A, W and bias; they are bf16, once differentiable, and zero for rows and experts without slots.
     expected_slots as moe_w8a8_gemm.
 
-    The forward and the backward pass can be captured into a graph.  As with any autograd work, hold no
-    graph of an eager call of the same leaves while capturing: torch then waits on the eager call's
-    stream inside the capture, which ends the process."""
+    The align's tensors are kept for the backward pass: buffers that a later batch's align writes over
+    must not be among them.  The forward and the backward pass can be captured into a graph.  As with
+    any autograd work, hold no graph of an eager call of the same leaves while capturing: torch then
+    waits on the eager call's stream inside the capture, which ends the process."""
     sorted_ids, expert_ids, ntpp, slot_local = align
     if slot_local is None:
         raise ValueError("moe_experts_linear needs the align's slot_local_ids")
