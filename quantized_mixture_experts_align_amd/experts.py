@@ -305,9 +305,10 @@ class _ExpertsLinear(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         A, W, *align, slot_local = ctx.saved_tensors
-        # (a gradient may arrive broadcast or transposed, or with rows too close for 16-byte loads)
+        # (a gradient may arrive broadcast or transposed, or with rows that 16-byte loads cannot take: between
+        # 16-byte boundaries it may be contiguous already, as a part of a concatenation's is, so it is copied)
         if grad.stride(-1) != 1 or grad.stride(0) % 8 or grad.stride(0) < grad.shape[1] or grad.data_ptr() % 16:
-            grad = grad.contiguous()
+            grad = grad.clone(memory_format=torch.contiguous_format)
         dA = dW = db = None
         if ctx.needs_input_grad[0]:
             dA = torch.empty(A.shape, dtype=A.dtype, device=A.device)

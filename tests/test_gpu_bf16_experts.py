@@ -189,3 +189,30 @@ def test_a_captured_training_step_replays():
         torch.cuda.synchronize()
         for a, b in zip(grads, step()):
             assert torch.equal(a, b)
+
+
+def off_alignment(t, lead):
+    """t's values, contiguous, `lead` values behind a 16-byte boundary."""
+    v = torch.zeros(t.numel() + lead, dtype=t.dtype, device=t.device)[lead:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16 == 2 * lead
+    return v
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_contiguous_gradients_off_16_byte_boundaries(gather):
+    """Contiguous gradients that begin between 16-byte boundaries, as the parts of a concatenation's do."""
+    M, k, E, N, K, B = 33, 2, 4, 40, 24, 16
+    top_k = k if gather else 1
+    al, _ = aligned(routing(M, k, E + 1, E, 2), 0, E, B)
+    leaves = [t.cuda().requires_grad_(True) for t in (bf16((M * k // top_k, K), 1), bf16((E, N, K), 2), bf16((E, N), 3))]
+    g = bf16((M * k, N), 4).cuda()
+    out = P.moe_experts_linear(leaves[0], leaves[1], al, top_k, B, bias=leaves[2])
+    want = torch.autograd.grad(out, leaves, g, retain_graph=True)
+    for lead in (1, 4):
+        got = torch.autograd.grad(out, leaves, off_alignment(g, lead), retain_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), lead
+    front = torch.zeros(4, dtype=torch.bfloat16, device="cuda")
+    joined = torch.cat([front, out.flatten()])
+    got = torch.autograd.grad(joined, leaves, torch.cat([front, g.flatten()]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
