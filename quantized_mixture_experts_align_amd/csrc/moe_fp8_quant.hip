@@ -35,9 +35,27 @@ struct QuantArgs {
 struct NoAct {
   float alpha, limit;
 };
+// Relu2 and SwigluAlpha with comparisons in the place of fminf and fmaxf, which return the other operand
+// for a NaN: here it stays one and becomes a NaN code.
+struct Relu2Nan {
+  float alpha, limit;
+  __device__ __forceinline__ float operator()(float h) const {
+    const float r = h < 0.0f ? 0.0f : h;
+    return r * r;
+  }
+};
+struct SwigluNan {
+  float alpha, limit;
+  __device__ __forceinline__ float operator()(float g, float u) const {
+    g = g > limit ? limit : g;
+    u = u < -limit ? -limit : u;
+    u = u > limit ? limit : u;
+    return g * sigmoid_f(alpha * g) * (u + 1.0f);
+  }
+};
 template <typename ACT> struct is_gated { static constexpr bool value = true; };
 template <> struct is_gated<NoAct> { static constexpr bool value = false; };
-template <> struct is_gated<Relu2> { static constexpr bool value = false; };
+template <> struct is_gated<Relu2Nan> { static constexpr bool value = false; };
 
 template <typename ACT>
 __global__ __launch_bounds__(256) void fp8_quant_kernel(QuantArgs a, ACT act) {
@@ -145,6 +163,6 @@ extern "C" int moe_act_fp8_quant(moe_act_kind kind, const uint16_t* h, int64_t l
                             slot_local_ids, codes, ld_codes, scales, ld_scales, &a, &empty);
   if (rc || empty) return rc;
   if (kind == MOE_ACT_SILU_MUL) return launch_quant("moe_act_fp8_quant", a, SiluMul{alpha, limit}, stream);
-  if (kind == MOE_ACT_RELU2) return launch_quant("moe_act_fp8_quant", a, Relu2{alpha, limit}, stream);
-  return launch_quant("moe_act_fp8_quant", a, SwigluAlpha{alpha, limit}, stream);
+  if (kind == MOE_ACT_RELU2) return launch_quant("moe_act_fp8_quant", a, Relu2Nan{alpha, limit}, stream);
+  return launch_quant("moe_act_fp8_quant", a, SwigluNan{alpha, limit}, stream);
 }

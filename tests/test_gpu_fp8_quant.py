@@ -105,3 +105,26 @@ def test_dropped_rows_strides_and_activations(kind, cols):
 def test_no_rows():
     codes, scales = P.moe_fp8_quant(torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"))
     assert codes.shape == (0, 256) and scales.shape == (0, 2)
+
+
+@pytest.mark.parametrize("kind,cols", [("silu_mul", 2), ("swiglu_alpha", 2), ("relu2", 1)])
+@pytest.mark.parametrize("limit", [4.0, float("inf")])
+def test_a_nan_before_the_activation_is_a_nan_code(kind, cols, limit):
+    """Codes and scales of rows with NaNs are those with a gate of 0 (whose activation is 0) in their place,
+    but for NaN codes there: a clamp or a maximum does not turn a NaN into a number."""
+    R, I = 21, 328
+    h = bf16((R, cols * I), 17, 3.0)
+    at = torch.from_numpy(np.random.default_rng(18).random((R, I)) < 0.05)
+    at[3, :128] = True                                    # a whole group
+    at[4] = False
+    clean = h.clone()
+    clean[:, :I][at] = 0
+    gate, up = h.clone(), h.clone()
+    gate[:, :I][at] = float("nan")
+    up[:, (cols - 1) * I:][at] = -float("nan")
+    want_c, want_s = (t.cpu() for t in P.moe_act_fp8_quant(kind, clean.cuda(), I, alpha=1.5, limit=limit))
+    for x in (gate, up):
+        codes, scales = (t.cpu() for t in P.moe_act_fp8_quant(kind, x.cuda(), I, alpha=1.5, limit=limit))
+        assert torch.equal(scales, want_s)
+        assert torch.equal(torch.isnan(codes.float()), at)
+        assert torch.equal(codes.view(torch.uint8)[~at], want_c.view(torch.uint8)[~at])
