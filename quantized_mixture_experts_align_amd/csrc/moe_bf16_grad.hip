@@ -19,7 +19,7 @@ struct GradArgs {
   int64_t ld_dc;
   const uint16_t* A;
   int64_t lda;
-  void* dW;            // [E, N, K]
+  void* dW;            // [E, N, K], or null: only dbias, from one strip of columns whose product is not stored
   void* dbias;         // [E, N] or null
   const int32_t* sorted;
   const int32_t* eids;
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
   const uint32_t ids_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int*)&s_ids[0][0][0];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = w / WN, wn = w % WN;
-  const int ks = (a.K + BN - 1) / BN, ns = (a.N + BM - 1) / BM;
+  const int ks = a.dW ? (a.K + BN - 1) / BN : 1, ns = (a.N + BM - 1) / BM;
   const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
 
   // The align lists the experts' blocks in rising order, so the counts of their blocks give their ranges.
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(GradArgs a) {
     }
     store_tiles<NG, MG, OUT>(acc, MG, s_out, w, lane, t.k0 + wn * 16 * NG, a.K, true, [&](int r) -> OUT* {
       const int n = t.n0 + wm * 16 * MG + r;
-      return n < a.N ? static_cast<OUT*>(a.dW) + ((int64_t)t.e * a.N + n) * a.K : nullptr;
+      return n < a.N && a.dW ? static_cast<OUT*>(a.dW) + ((int64_t)t.e * a.N + n) * a.K : nullptr;
     });
     if (last) break;
     wait_vm<0>();
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
 template <typename OUT, int MG, int NG, int WM, int WN>
 static int launch_wgrad_tile(const char* fn, GradArgs a, int per_cu, hipStream_t st) {
   constexpr int BM = 16 * MG * WM, BN = 16 * NG * WN;
-  const int64_t tiles = (int64_t)((a.N + BM - 1) / BM) * a.E, strips = (a.K + BN - 1) / BN;
+  const int64_t tiles = (int64_t)((a.N + BM - 1) / BM) * a.E, strips = a.dW ? (a.K + BN - 1) / BN : 1;
   const int64_t positions = choose_units(tiles, strips, &a.group_m, &a.group_n);
   MOE_REQUIRE(positions < (1ll << 30), MOE_EUNSUPPORTED, "%s: grid too large", fn);
   a.positions = (int32_t)positions;
@@ -310,7 +310,7 @@ static int launch_wgrad_tile(const char* fn, GradArgs a, int per_cu, hipStream_t
 // them, 27 and 20 us).
 template <typename OUT>
 static int launch_wgrad(const char* fn, const GradArgs& a, hipStream_t st) {
-  if ((int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E >= device_cu_count())
+  if ((int64_t)((a.N + 255) / 256) * (a.dW ? (a.K + 255) / 256 : 1) * a.E >= device_cu_count())
     return launch_wgrad_tile<OUT, 8, 4, 2, 4>(fn, a, 1, st);
   return launch_wgrad_tile<OUT, 4, 2, 2, 4>(fn, a, 2, st);
 }
@@ -378,11 +378,18 @@ extern "C" int moe_bf16_gemm_wgrad(const uint16_t* dC, int64_t ld_dc, const uint
   const char* fn = "moe_bf16_gemm_wgrad";
   int rc = check_grad(fn, dC, ld_dc, E, N, K, numel, top_k, block_m);
   if (rc) return rc;
+  if (!dW) {  // the bias alone: dC takes the place of A too (the bias's sums are the same; A is not looked at)
+    A = dC;
+    a_rows = numel;
+    lda = ld_dc;
+    K = N;
+    top_k = 1;
+  }
   MOE_REQUIRE(a_rows >= numel / top_k, MOE_EINVAL, "%s: A has %lld rows, slots need %lld", fn, (long long)a_rows,
               (long long)(numel / top_k));
   MOE_REQUIRE(lda >= K && lda % 8 == 0, MOE_EINVAL, "%s: lda=%lld (>= K=%d, multiple of 8)", fn, (long long)lda, K);
-  MOE_REQUIRE(dW && num_tokens_post_padded && (numel == 0 || (A && sorted_token_ids && expert_ids)), MOE_EINVAL,
-              "%s: null pointer", fn);
+  MOE_REQUIRE((dW || dbias) && num_tokens_post_padded && (numel == 0 || (A && sorted_token_ids && expert_ids)),
+              MOE_EINVAL, "%s: null pointer", fn);
   MOE_REQUIRE((((uintptr_t)A | (uintptr_t)dW) & 15) == 0 && ((uintptr_t)dbias & 3) == 0, MOE_EUNSUPPORTED,
               "%s: misaligned pointer (A and dW 16 B, dbias 4 B)", fn);
   int64_t cap = 0, cap_blocks = 0;

@@ -223,9 +223,11 @@ def _dgrad(dC, W, sorted_ids, expert_ids, ntpp, live: int, top_k, block_m, out, 
 
 
 def _wgrad(dC, A, E, sorted_ids, expert_ids, ntpp, top_k, block_m, out, out_bias) -> None:
+    dtype = (out_bias if out is None else out).dtype
     _call(dC.device, "moe_bf16_gemm_wgrad", dC.data_ptr(), _ld(dC), A.data_ptr(), A.shape[0], _ld(A), E, dC.shape[1],
-          A.shape[1], out.data_ptr(), None if out_bias is None else out_bias.data_ptr(), int(out.dtype is torch.float32),
-          sorted_ids.data_ptr(), expert_ids.data_ptr(), ntpp.data_ptr(), dC.shape[0], top_k, block_m)
+          A.shape[1], None if out is None else out.data_ptr(), None if out_bias is None else out_bias.data_ptr(),
+          int(dtype is torch.float32), sorted_ids.data_ptr(), expert_ids.data_ptr(), ntpp.data_ptr(), dC.shape[0], top_k,
+          block_m)
 
 
 def moe_bf16_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, sorted_token_ids: torch.Tensor, expert_ids: torch.Tensor,
@@ -298,7 +300,7 @@ class _ExpertsLinear(torch.autograd.Function):
         out = moe_bf16_gemm(A, W, sorted_ids, expert_ids, ntpp, slot_local.numel(), top_k, block_m, bias=bias,
                             expected_slots=expected, slot_local_ids=slot_local)
         ctx.save_for_backward(A, W, sorted_ids, expert_ids, ntpp, slot_local)
-        ctx.top_k, ctx.block_m, ctx.expected, ctx.has_bias = top_k, block_m, expected, bias is not None
+        ctx.top_k, ctx.block_m, ctx.expected = top_k, block_m, expected
         return out
 
     @staticmethod
@@ -315,8 +317,9 @@ class _ExpertsLinear(torch.autograd.Function):
             work = None if ctx.top_k == 1 else torch.empty(grad.shape[0] * W.shape[2], dtype=torch.float32, device=A.device)
             _dgrad(grad, W, *align, slot_local.data_ptr(), ctx.top_k, ctx.block_m, dA, work, ctx.expected)
         if ctx.needs_input_grad[1] or ctx.needs_input_grad[2]:
-            dW = torch.empty_like(W)
-            if ctx.has_bias and ctx.needs_input_grad[2]:
+            if ctx.needs_input_grad[1]:
+                dW = torch.empty_like(W)
+            if ctx.needs_input_grad[2]:
                 db = torch.empty(W.shape[:2], dtype=W.dtype, device=W.device)
             _wgrad(grad, A, W.shape[0], *align, ctx.top_k, ctx.block_m, dW, db)
         return dA, dW, db, None, None, None, None, None, None, None

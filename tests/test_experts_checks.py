@@ -102,3 +102,11 @@ def test_experts_linear_checks_its_rows():
         P.moe_experts_linear(torch.zeros((3, 8)), torch.zeros((1, 8, 8)), align, 2, 16)
     with pytest.raises(ValueError, match="slot_local_ids"):
         P.moe_experts_linear(torch.zeros((4, 8)), torch.zeros((1, 8, 8)), (None, None, None, None), 2, 16)
+
+
+def test_the_bias_gradient_alone_needs_no_rows():
+    f = L.lib().moe_bf16_gemm_wgrad
+    alone = {**WGRAD, **dict(A=None, a_rows=0, lda=0, dW=None, dbias=A16)}
+    for change, code in ((dict(dbias=A16 + 2), L.MOE_EUNSUPPORTED), (dict(dbias=None), L.MOE_EINVAL),
+                         (dict(ntpp=None), L.MOE_EINVAL), (dict(dC=None), L.MOE_EINVAL), (dict(ld_dc=120), L.MOE_EINVAL)):
+        assert f(*{**alone, **change}.values()) == code, change

@@ -216,3 +216,27 @@ def test_contiguous_gradients_off_16_byte_boundaries(gather):
     joined = torch.cat([front, out.flatten()])
     got = torch.autograd.grad(joined, leaves, torch.cat([front, g.flatten()]))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# (N = 8192: 256-row tiles of an expert's columns; the others 128-row ones)
+@pytest.mark.parametrize("M,k,E,N,K,B", [(33, 2, 4, 40, 24, 16), (300, 3, 5, 264, 520, 64), (260, 2, 8, 8192, 256, 32),
+                                         (1, 1, 1, 8, 8, 16)])
+@pytest.mark.parametrize("gather", [True, False])
+def test_the_bias_gradient_alone(M, k, E, N, K, B, gather):
+    """Frozen weights: the same bits as beside the weights' gradient, which is neither made nor stored."""
+    top_k = k if gather else 1
+    al, _ = aligned(routing(M, k, E + 1, E, 2), 0, E, B)
+    A, W, b = bf16((M * k // top_k, K), 1).cuda(), bf16((E, N, K), 2).cuda(), bf16((E, N), 3).cuda().requires_grad_(True)
+    g = bf16((M * k, N), 4).cuda()
+    _, want = P.moe_bf16_gemm_wgrad(g, A, E, *al[:3], top_k, B, bias_grad=True)
+    out = P.moe_experts_linear(A, W, al, top_k, B, bias=b)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    (got,) = torch.autograd.grad(out, b, g)
+    assert torch.equal(got, want)
+    assert W.numel() < 4096 or torch.cuda.max_memory_allocated() - before < 2 * W.numel()
+    # and with the rows' gradient
+    A.requires_grad_(True)
+    dA, db = torch.autograd.grad(P.moe_experts_linear(A, W, al, top_k, B, bias=b), (A, b), g)
+    assert torch.equal(db, want) and torch.equal(dA, P.moe_bf16_gemm_dgrad(g, W, *al, top_k, B))
