@@ -354,6 +354,7 @@ extern "C" int moe_bf16_gemm_dgrad(const uint16_t* dC, int64_t ld_dc, const uint
               MOE_EINVAL, "%s: null pointer", fn);
   MOE_REQUIRE((((uintptr_t)W | (uintptr_t)dA | (uintptr_t)work) & 15) == 0, MOE_EUNSUPPORTED,
               "%s: misaligned pointer (16 B)", fn);
+  MOE_REQUIRE(top_k == 1 || launchable(numel / top_k, 256), MOE_EUNSUPPORTED, "%s: grid too large", fn);
   int64_t cap = 0, cap_blocks = 0;
   rc = moe_align_capacity(numel, 1, E, block_m, &cap, &cap_blocks);
   if (rc) return rc;

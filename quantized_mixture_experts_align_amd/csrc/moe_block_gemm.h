@@ -101,6 +101,9 @@ __device__ __forceinline__ int slot_at(const BlockGemmArgs& a, int64_t at) {
   return s >= 0 && s < a.numel ? (int)s : -1;
 }
 
+// A launch counts its threads in 32 bits.
+inline bool launchable(int64_t grid, int threads) { return grid * threads < (1ll << 32); }
+
 // Zeros in the rows of dropped slots, shared by all the workgroups of a launch: rows blockIdx.x, +
 // gridDim.x, ..., of which `mine` holds the flags of the first 64 (asked for when the workgroup starts,
 // as drop_flags, so that its end does not wait for them).
@@ -265,7 +268,7 @@ template <typename T, int NG, int KS, int MB>
 static int launch_stream(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipStream_t st) {
   a.cap_blocks = (int32_t)cap_blocks;
   const int64_t grid = (int64_t)((a.N + 16 * NG - 1) / (16 * NG)) * cap_blocks;
-  MOE_REQUIRE(grid < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+  MOE_REQUIRE(launchable(grid, 64 * KS), MOE_EUNSUPPORTED, "%s: grid too large", fn);
   hipLaunchKernelGGL((block_gemm_stream_kernel<T, NG, KS, MB>), dim3((unsigned)grid), dim3(64 * KS), 0, st, a);
   return check_launch(fn);
 }
@@ -793,7 +796,7 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
   const int64_t tiles = kMerge ? merged_tiles(a, cap_blocks, BM) : cap_blocks * ((a.block_m + BM - 1) / BM);
   const int64_t grid = choose_units(tiles, (a.N + BN - 1) / BN, &a.group_m, &a.group_n);
   a.tiles = (int32_t)tiles;
-  MOE_REQUIRE(grid < (1ll << 31) && tiles < (1ll << 31), MOE_EUNSUPPORTED, "%s: grid too large", fn);
+  MOE_REQUIRE(launchable(grid, 64 * WM * WN), MOE_EUNSUPPORTED, "%s: grid too large", fn);  // (tiles <= grid)
   hipLaunchKernelGGL((block_gemm_tile_kernel<T, MG, NG, WM, WN, kStages, kMerge>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, a);
   return check_launch(fn);

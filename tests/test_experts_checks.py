@@ -110,3 +110,17 @@ def test_the_bias_gradient_alone_needs_no_rows():
     for change, code in ((dict(dbias=A16 + 2), L.MOE_EUNSUPPORTED), (dict(dbias=None), L.MOE_EINVAL),
                          (dict(ntpp=None), L.MOE_EINVAL), (dict(dC=None), L.MOE_EINVAL), (dict(ld_dc=120), L.MOE_EINVAL)):
         assert f(*{**alone, **change}.values()) == code, change
+
+
+# A launch has fewer than 2^32 threads: streamed blocks; tiles of 32 to 256 rows; the sum over a row's slots
+@pytest.mark.parametrize("name,good,change", [
+    ("moe_bf16_gemm", BF16, dict(numel=1 << 25, a_rows=1 << 25, N=8192, ldc=8192)),
+    ("moe_w8a8_gemm", W8A8, dict(numel=1 << 25, a_rows=1 << 25, N=8192, ldc=8192)),
+    ("moe_bf16_gemm", BF16, dict(numel=1 << 28, a_rows=1 << 28, N=8192, ldc=8192, block_m=32)),
+    ("moe_bf16_gemm", BF16, dict(numel=1 << 29, a_rows=1 << 29, N=8192, ldc=8192, block_m=128)),
+    ("moe_w8a8_linear", LINEAR, dict(M=1 << 29, N=8192, ldc=8192)),
+    ("moe_bf16_gemm_dgrad", DGRAD, dict(numel=1 << 26, N=8, K=8, ld_dc=8, ld_da=8, block_m=256, work_elems=1 << 29)),
+    ("moe_bf16_gemm_dgrad", DGRAD, dict(numel=1 << 29, N=8, K=8192, ld_dc=8, ld_da=8192, top_k=1, block_m=64))])
+def test_launches_of_too_many_threads_are_refused(name, good, change):
+    assert getattr(L.lib(), name)(*{**good, **change}.values()) == L.MOE_EUNSUPPORTED
+    assert b"grid too large" in L.lib().moe_last_error()
