@@ -241,3 +241,18 @@ def test_captured_products_follow_the_routing(B):
         torch.cuda.synchronize()
         for x, y in zip(out, run()):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("B,expected", [(16, 0), (16, 1), (16, 10000), (32, 0), (128, 0)])
+def test_stale_entries_behind_the_live_blocks_of_the_8_bit_product(B, expected):
+    M, k, E, N, K = 300, 2, 6, 520, 272
+    al, local = aligned(skewed(M, k, E, 3), 0, E, B)
+    s, e, n, _ = (t.clone() for t in al)
+    live = int(n)
+    a, sa, w, sb = (t.cuda() for t in (e4m3((M, K), 1), scales((M, 3), 1), e4m3((E, N, K), 2), scales((E, 5, 3), 2)))
+    run = lambda s, e: P.moe_w8a8_gemm(a, sa, w, sb, s, e, n, M * k, k, B, expected_slots=expected)  # noqa: E731
+    want = run(al[0], al[1])
+    s[live:], e[live // B:] = 5, int(e[live // B - 1])                # a live slot; the last block's expert
+    assert torch.equal(run(s, e), want)
+    e[live // B:] = 1 << 30
+    assert torch.equal(run(s, e), want)
