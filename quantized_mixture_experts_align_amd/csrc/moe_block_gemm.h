@@ -38,7 +38,7 @@ struct BlockGemmArgs {
   int32_t tiles, group_m, group_n;  // tile kernel: tiles of rows; tiles and strips of an XCD's unit
   int32_t cap_blocks;     // most blocks the align can have made
   const int32_t* live;    // set: rows of C whose slot is dropped (live[slot] < 0) are zeroed, else left alone
-  int64_t expected;       // live slots to expect: chooses the launch, never a result
+  int64_t expected;       // live slots to expect: chooses the launch, hence the order of sums, and nothing else
 };
 
 struct Fp8Type {
@@ -132,7 +132,7 @@ __device__ __forceinline__ void zero_dropped(const BlockGemmArgs& a, int mine) {
 // Workgroup = up to 16 slots of a block (MB = 2: of two consecutive blocks of one expert) x NG 16-row
 // weight tiles, K split over its KS waves, operands straight from memory to registers in chunks of
 // kChunk steps, partial sums joined through LDS in wave order.  The cost is the stream of weights (64 tokens
-// of 8 choices on 32 of 256 experts, N = 8192, K = 4096: 142 us, 6.6 TB/s).
+// of 8 choices on 32 of 256 experts, N = 8192, K = 4096: 876 MB in 147 - 150 us, 5.8 - 6.0 TB/s).
 template <typename T, int NG, int KS, int MB>
 __device__ __forceinline__ void gemm_stream(const BlockGemmArgs& a, f32x4_t (&part)[KS][NG * MB][64]) {
   constexpr int kChunk = 4;
@@ -816,6 +816,10 @@ static int launch_tile(const char* fn, BlockGemmArgs a, int64_t cap_blocks, hipS
 // made of an expert's 128-row blocks, counted in the kernel (2 us more), where the batch has 128 slots an
 // expert (1024 Zipf tokens of 8 choices on 32 of 256 experts: 618 us with 128 rows, 604 with 256; 4096 of
 // them 975 and 908).
+// Blocks of 17 to 32 rows run the 64-row shapes with half the rows, weighed by the 64-row ones' figures, counts and
+// residency (not fitted apart: up to twice as many tiles run, and LDS would hold three and two a CU).  K is split
+// over waves up to 16 rows only, so 17 to some 500 dense rows along a long K leave CUs idle (N = 4096, K = 7168: 16
+// rows 13 us, 17 to 256 21 - 27, 512 43).
 template <typename T>
 static int launch_block_gemm(const char* fn, const BlockGemmArgs& a, int64_t cap_blocks, hipStream_t st) {
   const int64_t cus = device_cu_count(), KT = (a.Kb + kStepBytes - 1) / kStepBytes;

@@ -3,6 +3,9 @@ point, with the same name, and moe_experts_linear, the differentiable form of mo
 
 Tensors are checked for device, type and shape, outputs allocated with torch when not given, and
 every computation runs in libmoe_w4a16 on the current stream of the tensors' device.
+
+block_m of the align: the least of 16, 32, 64 and 128 that holds a local expert's mean number of slots,
+128 above.  expected_slots: on a slice of the experts tokens * top_k * n_local / n_experts.
 """
 from __future__ import annotations
 
