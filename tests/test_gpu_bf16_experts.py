@@ -240,3 +240,35 @@ def test_the_bias_gradient_alone(M, k, E, N, K, B, gather):
     A.requires_grad_(True)
     dA, db = torch.autograd.grad(P.moe_experts_linear(A, W, al, top_k, B, bias=b), (A, b), g)
     assert torch.equal(db, want) and torch.equal(dA, P.moe_bf16_gemm_dgrad(g, W, *al, top_k, B))
+
+
+def test_the_bias_gradient_alone_of_no_tokens_and_in_a_graph():
+    E, N, K, B = 4, 264, 64, 16
+    W, b = bf16((E, N, K), 1).cuda(), bf16((E, N), 2).cuda().requires_grad_(True)
+    al = P.moe_align(torch.zeros((0, 2), dtype=torch.int32, device="cuda"), 0, E, B)
+    out = P.moe_experts_linear(torch.zeros((0, K), dtype=torch.bfloat16, device="cuda"), W, al, 2, B, bias=b)
+    (db,) = torch.autograd.grad(out, b, torch.zeros_like(out))
+    assert db.shape == b.shape and not bool(db.any())
+    del out                                                             # (no eager graph of b lives on)
+    M = 90
+    ids = torch.from_numpy(routing(M, 2, E, E, 3)).cuda()
+    A, g = bf16((M, K), 3).cuda(), bf16((2 * M, N), 4).cuda()
+
+    def step():
+        return torch.autograd.grad(P.moe_experts_linear(A, W, P.moe_align(ids, 0, E, B), 2, B, bias=b), b, g)[0]
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step()
+    for seed in (5, 6, 7):
+        g.copy_(bf16((2 * M, N), seed))
+        ids.copy_(torch.from_numpy(routing(M, 2, E, E, seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, step())
