@@ -13,6 +13,9 @@ from .ops import (align_capacity, choose_block_m, gemm_choose, gemm_occupancy, g
                   moe_w4a16_gemm_combine_noalloc)
 from .experts import (moe_act_fp8_quant, moe_bf16_gemm, moe_bf16_gemm_dgrad, moe_bf16_gemm_wgrad, moe_experts_linear,
                       moe_fp8_quant, moe_w8a8_gemm, moe_w8a8_linear)
+from .router import (RouterStats, Routing, combine_grad_workspace, moe_combine_grad, moe_experts_combine,
+                     moe_experts_router, moe_router, moe_router_grad, router_workspace)
+from .adapters import adapters_workspace, moe_adapters_add
 from .layer import MoELayer, Workspace
 
 __all__ = [
@@ -23,5 +26,7 @@ __all__ = [
     "requant_config", "moe_permute_cols", "moe_w4a16_gemm_combine", "combine_counters",
     "moe_w4a16_gemm_combine_noalloc", "moe_fp8_quant", "moe_act_fp8_quant", "moe_w8a8_gemm",
     "moe_w8a8_linear", "moe_bf16_gemm", "moe_bf16_gemm_dgrad", "moe_bf16_gemm_wgrad",
-    "moe_experts_linear",
+    "moe_experts_linear", "moe_router", "moe_router_grad", "moe_experts_router", "RouterStats", "Routing",
+    "router_workspace", "moe_combine_grad", "moe_experts_combine", "combine_grad_workspace", "moe_adapters_add",
+    "adapters_workspace",
 ]

@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_w4a16.so")
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ESIZE, MOE_EHIP = 0, -1, -2, -3, -4
 QTYPE = {"int4_g128": 0, "nvfp4_g16": 1, "mxfp4_g32": 2, "int4zp_g128": 3, "int4zpf_g128": 4}
 ACT = {"silu_mul": 0, "swiglu_alpha": 1, "relu2": 2}
+SCORE = {"softmax": 0, "sigmoid": 1}
 GATED = {"silu_mul": True, "swiglu_alpha": True, "relu2": False}
 PREP_GATE_UP, PREP_INTERLEAVED, PREP_PAD, PREP_ACT_ORDER = 0x1, 0x2, 0x4, 0x8
 GEMM_AUTO, GEMM_DECODE, GEMM_MFMA = 0, 1, 2
@@ -88,6 +89,16 @@ SIGNATURES = {
                                       _I32, _I64, _P, _I64, _P]),
     "moe_bf16_gemm_wgrad": (C.c_int, [_P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P,
                                       _I64, _I32, _I32, _P]),
+    "moe_router_workspace": (C.c_int, [_I64, _I32, C.POINTER(_I64)]),
+    "moe_router": (C.c_int, [_P, _I32, _I64, _I64, _I32, _P, _P, C.c_int, _I32, _I32, _F, _P, _P, _P, _P, _P, _P, _P,
+                             _I64, _P]),
+    "moe_router_grad": (C.c_int, [_P, _I32, _I64, _I64, _I32, _P, C.c_int, _I32, _I32, _F, _P, _P, _P, _P, _P, _P, _P,
+                                  _I64, _P]),
+    "moe_combine_grad_workspace": (C.c_int, [_I64, _I32, C.POINTER(_I64)]),
+    "moe_combine_grad": (C.c_int, [_P, _P, _P, _P, _F, _F, _I64, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I64, _P]),
+    "moe_adapters_workspace": (C.c_int, [_I64, _I32, _I32, _I32, _I32, C.POINTER(_I64)]),
+    "moe_adapters_add": (C.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _P, _P,
+                                   _P, _P, _I64, _I32, _I32, _P, _I64, _P]),
 }
 
 _lib = None
