@@ -94,7 +94,7 @@ BAD = [
                                           {**STATS, "tokens": None}]),
     ("moe_router", ROUTER, L.MOE_EUNSUPPORTED, [dict(E=1025, ld=1025), dict(top_k=17), dict(M=(1 << 25) + 1), dict(logits=A16 + 1),
                                                 dict(logits=A16 + 2, f32=1), dict(ids=A16 + 2), dict(weights=A16 + 2),
-                                                dict(bias=A16 + 2), dict(live=A16 + 2), {**STATS, "work": A16 + 2}]),
+                                                dict(bias=A16 + 2), dict(live=A16 + 2), {**STATS, "work": A16 + 4}]),
     ("moe_router", ROUTER, L.MOE_ESIZE, [{**STATS, "work_bytes": 16 + 8 * 64 + 3}]),
     ("moe_router_grad", GRAD, L.MOE_EINVAL, [dict(logits=None), dict(dx=None), dict(ids=None), dict(counts=None),
                                              dict(tokens=None), dict(ld_d=63), dict(ld=60), dict(score=5), dict(top_k=0)]),
@@ -139,10 +139,10 @@ def test_empty_batches_launch_nothing():
 
 
 def test_workspace_sizes():
-    # statistics: a counter, and for each of at most 256 workgroups of 16 tokens (4 above 512 experts) E sums and counts
+    # statistics: the totals, and for each of at most 256 workgroups of 32 tokens (8 above 512 experts) E sums and counts
     # and its tokens
     assert P.router_workspace(1, 8) == 16 + 8 * 8 + 4
-    assert P.router_workspace(33, 256) == 16 + 3 * (8 * 256 + 4)
+    assert P.router_workspace(65, 256) == 16 + 3 * (8 * 256 + 4)
     assert P.router_workspace(1 << 20, 1024) == 16 + 256 * (8 * 1024 + 4)
     assert P.router_workspace(0, 8) == P.router_workspace(1, 8)
     # the inner products of every row, times at most 32 for short batches
