@@ -8,6 +8,7 @@
 // Bound: memory (every live row of y is read once, every row of dy written once).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_internal.h"
 
@@ -140,20 +141,223 @@ __global__ __launch_bounds__(kCgThreads) void combine_grad_kernel(CombineGradArg
       for (int j = 0; j < 8; ++j) a.part[(int64_t)blockIdx.x * a.H + c * 8 + j] = dn[c * 8 + j];
 }
 
-// The workgroups' partial sums of dn: 32 columns a workgroup, eight threads to a column.
-__global__ __launch_bounds__(256) void combine_dnorm_kernel(const float* part, int parts, int32_t H, uint16_t* dn) {
-  const int col = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
-  __shared__ float red[8][33];
-  float s = 0.0f;
-  if (c < H)
-    for (int p = row; p < parts; p += 8) s += part[(int64_t)p * H + c];
-  red[row][col] = s;
-  __syncthreads();
-  if (row == 0 && c < H) {
-    s = 0.0f;
-    for (int i = 0; i < 8; ++i) s += red[i][col];
-    dn[c] = f32_to_bf16(s);
+// ---------------------------------------------------------------------------- one pass in registers
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+
+// Sums of N values (a power of two) over the 64 lanes.  Halves of two values change places, then quarters, so that one
+// register goes on with both sums: N + N / 2 exchanges and 4 N / 4 rotations in the place of 6 N.  Lane 16 r then holds in
+// v[i] the sum of value 4 i + 2 (r & 1) + (r >> 1) (N >= 4), 2 (r & 1) of N = 2 in its first bit r >> 1, ...
+template <int N>
+__device__ __forceinline__ void wave_sums(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < (N + 1) / 2; ++i) {
+    const uint32_t a = __float_as_uint(v[N > 1 ? 2 * i : 0]), b = __float_as_uint(v[N > 1 ? 2 * i + 1 : 0]);
+    const u32x2_t s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
   }
+  constexpr int N2 = (N + 1) / 2;
+#pragma unroll
+  for (int i = 0; i < (N2 + 1) / 2; ++i) {
+    const uint32_t a = __float_as_uint(v[N2 > 1 ? 2 * i : 0]), b = __float_as_uint(v[N2 > 1 ? 2 * i + 1 : 0]);
+    const u32x2_t s = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  constexpr int N4 = (N2 + 1) / 2;
+#pragma unroll
+  for (int i = 0; i < N4; ++i) {
+    v[i] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v[i]), 0x128, 0xf, 0xf, false));
+    v[i] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v[i]), 0x124, 0xf, 0xf, false));
+    v[i] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v[i]), 0x122, 0xf, 0xf, false));
+    v[i] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v[i]), 0x121, 0xf, 0xf, false));
+  }
+}
+
+// For top_k <= TK and rows of at most CP * blockDim.x chunks of 8 columns: a token's operands are asked for at once (with
+// `spec` before its flags are known; what dead rows hold is never used) and stay in registers between the sums and the
+// rows of dy.  Every wave makes the slots' factors of the workgroup's sums for itself, and tokens alternate between two
+// places for the sums, so that a token costs one barrier.
+template <bool NORM, int TK, int CP>
+__global__ __launch_bounds__(512) void combine_grad1_kernel(CombineGradArgs a, int spec) {
+  constexpr int N = NORM ? 2 * TK : TK, N4 = N >= 4 ? N / 4 : 1;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, T = blockDim.x, W = T / 64;
+  const int chunks = a.H >> 3;
+  __shared__ float red[2][8][N];
+  float dn[NORM ? CP : 1][8];
+#pragma unroll
+  for (int c = 0; c < (NORM ? CP : 1); ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dn[c][j] = 0.0f;
+  uint4 nv[CP];
+#pragma unroll
+  for (int c = 0; c < CP; ++c) {
+    nv[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (NORM && tid + c * T < chunks) nv[c] = *reinterpret_cast<const uint4*>(a.nw + (tid + c * T) * 8);
+  }
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.M; t += gridDim.x, turn ^= 1) {
+    uint32_t live = 0;
+    float g[TK];
+#pragma unroll
+    for (int s = 0; s < TK; ++s) {
+      g[s] = 0.0f;
+      if (s < a.k) {
+        g[s] = a.gw[t * a.k + s];
+        if (a.local[t * a.k + s] >= 0) live |= 1u << s;
+      }
+    }
+    uint4 y[TK][CP], go[CP];
+    float sum[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {
+      const int col = tid + c * T;
+      go[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (col < chunks) go[c] = *reinterpret_cast<const uint4*>(a.dout + t * a.ldd + col * 8);
+#pragma unroll
+      for (int s = 0; s < TK; ++s) {
+        y[s][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (s < a.k && col < chunks && (spec || ((live >> s) & 1)))
+          y[s][c] = *reinterpret_cast<const uint4*>(a.y + (t * a.k + s) * (int64_t)a.H + col * 8);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {
+      float gv[8], n8[8];
+      unpack8(go[c], gv);
+      if (NORM) unpack8(nv[c], n8);
+#pragma unroll
+      for (int s = 0; s < TK; ++s) {
+        if (!((live >> s) & 1)) continue;
+        float yv[8];
+        unpack8(y[s][c], yv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float z = NORM ? yv[j] * n8[j] : yv[j];
+          sum[s] = fmaf(gv[j], z, sum[s]);
+          if constexpr (NORM) sum[TK + s] = fmaf(z, z, sum[TK + s]);
+        }
+      }
+    }
+    wave_sums<N>(sum);
+    if ((lane & 15) == 0) {
+      const int r = lane >> 4;
+#pragma unroll
+      for (int i = 0; i < N4; ++i) {
+        const int at = N >= 4 ? 4 * i + 2 * (r & 1) + (r >> 1) : r >> 1;
+        if (at < N) red[turn][wv][at] = sum[i];
+      }
+    }
+    __syncthreads();
+    // lane s: the factors of slot s
+    const int sl = lane < TK ? lane : 0;
+    float dot = 0.0f, ss = 0.0f, gs = 0.0f;
+    for (int i = 0; i < W; ++i) {
+      dot += red[turn][i][sl];
+      if constexpr (NORM) ss += red[turn][i][TK + sl];
+    }
+#pragma unroll
+    for (int s = 0; s < TK; ++s) gs = sl == s ? g[s] : gs;
+    const bool on = (live >> sl) & 1;
+    const float r = NORM ? 1.0f / sqrtf(ss / (float)a.H + a.eps) : 1.0f;
+    const float f0 = on ? a.rsf * gs * r : 0.0f, f1 = NORM && on ? r * r * dot / (float)a.H : 0.0f;
+    if (a.dg && wv == 0 && lane < a.k) a.dg[t * a.k + lane] = on ? a.rsf * r * dot : 0.0f;
+    if (!a.dy && !a.part) continue;
+    float p[TK], q[TK];  // (read from their lanes here, where all are active)
+#pragma unroll
+    for (int s = 0; s < TK; ++s) {
+      p[s] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f0), s));
+      q[s] = NORM ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f1), s)) : 0.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {
+      const int col = tid + c * T;
+      if (col >= chunks) break;
+      float gv[8], n8[8];
+      unpack8(go[c], gv);
+      if (NORM) unpack8(nv[c], n8);
+#pragma unroll
+      for (int s = 0; s < TK; ++s) {
+        if (s >= a.k) break;
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if ((live >> s) & 1) {
+          float dv[8];
+          if constexpr (NORM) {
+            float yv[8];
+            unpack8(y[s][c], yv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float dz = p[s] * fmaf(-q[s], yv[j] * n8[j], gv[j]);
+              dv[j] = dz * n8[j];
+              dn[c][j] = fmaf(dz, yv[j], dn[c][j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dv[j] = p[s] * gv[j];
+          }
+          o = pack8(dv);
+        }
+        if (a.dy) *reinterpret_cast<uint4*>(a.dy + (t * a.k + s) * (int64_t)a.H + col * 8) = o;
+      }
+    }
+  }
+  if constexpr (NORM) {
+    if (a.part) {
+#pragma unroll
+      for (int c = 0; c < CP; ++c) {
+        const int col = tid + c * T;
+        if (col >= chunks) break;
+        float4* o = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.H + col * 8);
+        o[0] = make_float4(dn[c][0], dn[c][1], dn[c][2], dn[c][3]);
+        o[1] = make_float4(dn[c][4], dn[c][5], dn[c][6], dn[c][7]);
+      }
+    }
+  }
+}
+
+template <bool NORM>
+static void launch_combine_grad1(const CombineGradArgs& a, unsigned grid, int T, int CP, int spec, hipStream_t st) {
+  auto go = [&](auto tk) {
+    constexpr int TK = decltype(tk)::value;
+    if (CP == 1) hipLaunchKernelGGL((combine_grad1_kernel<NORM, TK, 1>), dim3(grid), dim3(T), 0, st, a, spec);
+    else hipLaunchKernelGGL((combine_grad1_kernel<NORM, TK, 2>), dim3(grid), dim3(T), 0, st, a, spec);
+  };
+  if (a.k <= 2) go(std::integral_constant<int, 2>{});
+  else if (a.k <= 4) go(std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 8>{});
+}
+
+// The workgroups' partial sums of dn: 32 columns a workgroup, four to a thread and 32 threads to a column's rows, sixteen
+// loads of each in flight.
+__global__ __launch_bounds__(256) void combine_dnorm_kernel(const float* part, int parts, int32_t H, uint16_t* dn) {
+  const int col = (threadIdx.x & 7) * 4, row = threadIdx.x >> 3, c = blockIdx.x * 32 + col;
+  __shared__ float red[32][33];
+  if (parts == 0) {  // no tokens
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) dn[blockIdx.x * 32 + threadIdx.x] = 0;
+    return;
+  }
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float4 v[kCgParts / 32];
+#pragma unroll
+  for (int i = 0; i < kCgParts / 32; ++i)  // (H is a multiple of 8: four columns are there or none)
+    v[i] = *reinterpret_cast<const float4*>(part + (int64_t)min(row + i * 32, parts - 1) * H + min(c, H - 4));
+#pragma unroll
+  for (int i = 0; i < kCgParts / 32; ++i)
+    if (row + i * 32 < parts) {
+      s[0] += v[i].x;
+      s[1] += v[i].y;
+      s[2] += v[i].z;
+      s[3] += v[i].w;
+    }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[row][col + j] = s[j];
+  __syncthreads();
+  const int o = threadIdx.x >> 3, sub = threadIdx.x & 7;  // eight threads a column
+  float r = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r += red[sub * 4 + i][o];
+  for (int d = 4; d >= 1; d >>= 1) r += __shfl_xor(r, d);
+  if (sub == 0 && blockIdx.x * 32 + o < H) dn[blockIdx.x * 32 + o] = f32_to_bf16(r);
 }
 
 static int64_t combine_parts(int64_t M) { return std::min<int64_t>(M, kCgParts); }
@@ -185,9 +389,9 @@ extern "C" int moe_combine_grad(const uint16_t* y, const float* topk_weights, co
   if (M == 0 && !d_norm_w) return ok();
   MOE_REQUIRE(dy || d_weights || d_norm_w, MOE_EINVAL, "moe_combine_grad: no gradient asked for");
   MOE_REQUIRE(M == 0 || (y && topk_weights && slot_local_ids && d_out), MOE_EINVAL, "moe_combine_grad: null pointer");
-  MOE_REQUIRE((((uintptr_t)y | (uintptr_t)d_out | (uintptr_t)dy | (uintptr_t)norm_w) & 15) == 0 && ((uintptr_t)d_norm_w & 1) == 0 &&
-                  (((uintptr_t)topk_weights | (uintptr_t)slot_local_ids | (uintptr_t)d_weights | (uintptr_t)work) & 3) == 0,
-              MOE_EUNSUPPORTED, "moe_combine_grad: bf16 tensors must be 16-byte aligned, the others 4");
+  MOE_REQUIRE((((uintptr_t)y | (uintptr_t)d_out | (uintptr_t)dy | (uintptr_t)norm_w | (uintptr_t)work) & 15) == 0 && ((uintptr_t)d_norm_w & 1) == 0 &&
+                  (((uintptr_t)topk_weights | (uintptr_t)slot_local_ids | (uintptr_t)d_weights) & 3) == 0,
+              MOE_EUNSUPPORTED, "moe_combine_grad: bf16 tensors and the workspace must be 16-byte aligned, the others 4");
   const int64_t parts = combine_parts(M);
   if (d_norm_w)
     MOE_REQUIRE((work && work_elems >= parts * H) || parts == 0, MOE_ESIZE, "moe_combine_grad: workspace of %lld values, need %lld",
@@ -197,7 +401,12 @@ extern "C" int moe_combine_grad(const uint16_t* y, const float* topk_weights, co
   if (M > 0) {
     const unsigned grid = (unsigned)(d_norm_w ? parts : M);
     const size_t lds = d_norm_w ? (size_t)H * 4 : 0;
-    if (norm_w) hipLaunchKernelGGL(combine_grad_kernel<true>, dim3(grid), dim3(kCgThreads), lds, stream, a);
+    const int chunks = H / 8;
+    if (top_k <= 8 && chunks <= 1024) {  // (what two chunks a thread and eight slots hold in registers)
+      const int T = std::min(512, (chunks + 63) / 64 * 64), CP = (chunks + T - 1) / T, spec = M <= 256;
+      if (norm_w) launch_combine_grad1<true>(a, grid, T, CP, spec, stream);
+      else launch_combine_grad1<false>(a, grid, T, CP, spec, stream);
+    } else if (norm_w) hipLaunchKernelGGL(combine_grad_kernel<true>, dim3(grid), dim3(kCgThreads), lds, stream, a);
     else hipLaunchKernelGGL(combine_grad_kernel<false>, dim3(grid), dim3(kCgThreads), lds, stream, a);
   }
   if (d_norm_w)

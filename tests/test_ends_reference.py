@@ -104,7 +104,7 @@ BAD = [
                                                  dict(norm=None), dict(dy=None, dw=None, dn=None)]),
     ("moe_combine_grad", COMBINE, L.MOE_EUNSUPPORTED, [dict(H=60), dict(H=0), dict(top_k=0), dict(top_k=17), dict(M=-1), dict(M=1 << 24),
                                                        dict(ld=68), dict(y=A16 + 8), dict(dout=A16 + 8), dict(dy=A16 + 8),
-                                                       dict(norm=A16 + 8), dict(dn=A16 + 1), dict(work=A16 + 2)]),
+                                                       dict(norm=A16 + 8), dict(dn=A16 + 1), dict(work=A16 + 8)]),
     ("moe_combine_grad", COMBINE, L.MOE_ESIZE, [dict(elems=4 * 64 - 1), dict(work=None)]),
     ("moe_adapters_add", ADAPT, L.MOE_EINVAL, [dict(base=None), dict(x=None), dict(A=None), dict(B=None), dict(out=None),
                                                dict(sorted=None), dict(eids=None), dict(ntpp=None), dict(work=None),
