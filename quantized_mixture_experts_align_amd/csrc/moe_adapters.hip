@@ -17,10 +17,17 @@ namespace moe {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 
 constexpr int kAdMaxRank = 256;
 constexpr int kAdRankTile = 64;    // ranks of a workgroup of the first launch
 constexpr int kAdMaxSplits = 32;
+#ifndef ADG
+#define ADG 512
+#define ADS 1024
+#endif
+constexpr int kAdGroups = ADG;     // workgroups that the first launch is split up to
+constexpr int kAdStrips = ADS;    // and the second
 constexpr int kAdMaxAdapters = 512;
 
 struct AdapterArgs {
@@ -44,85 +51,133 @@ struct AdapterArgs {
 __device__ __forceinline__ int adapter_rank(const AdapterArgs& a, int ad) {
   return a.ranks ? min(max(a.ranks[ad], 0), a.r) : a.r;
 }
-// The row tile's adapter (-1: nothing to do) and the sorted position of its first row; `n` rows of the block
-// from there.
-__device__ __forceinline__ int row_tile(const AdapterArgs& a, int tile, int rows, int64_t& at, int& n) {
-  const int b = tile / a.per, sub = tile - b * a.per;
-  at = (int64_t)b * a.block_m + sub * rows;
-  n = min(rows, a.block_m - sub * rows);
-  if ((int64_t)b * a.block_m >= *a.padded) return -1;
-  const int ad = a.adapters[b];
-  return ad < a.L ? ad : -1;
-}
-__device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
-
-// t[split][m][j] = sum over the split's k of A[a, j, k] x[m / top_k, k].  MT x RT tiles of 16 rows x 16 ranks;
-// the four waves take every fourth step of 32 k and their sums meet in LDS.
-template <int MT, int RT>
-__global__ __launch_bounds__(256) void adapters_inner_kernel(AdapterArgs a) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
-  __shared__ f32x4_t red[3][MT * RT][64];
+// A row tile: its adapter (-1: nothing to do), the sorted position of its first row, its rows.  All of what it needs is
+// asked for at once; what stands behind the live blocks is looked at, never used.
+struct RowTile {
+  int adapter;
   int64_t at;
   int n;
-  const int ad = row_tile(a, blockIdx.x, 16 * MT, at, n);
-  if (ad < 0) return;
-  const int rank = adapter_rank(a, ad), r0 = blockIdx.z * kAdRankTile;
+};
+__device__ __forceinline__ RowTile row_tile(const AdapterArgs& a, int tile, int rows) {
+  const int b = tile / a.per, sub = tile - b * a.per;
+  RowTile w;
+  w.at = (int64_t)b * a.block_m + sub * rows;
+  w.n = min(rows, a.block_m - sub * rows);
+  const int ad = a.adapters[b], end = *a.padded;
+  w.adapter = (int64_t)b * a.block_m < end && ad < a.L ? ad : -1;
+  return w;
+}
+// The slot of the tile's row i, -1 for padding.
+__device__ __forceinline__ int slot_of(const AdapterArgs& a, const RowTile& w, int i) {
+  const int s = a.sorted[w.at + min(i, w.n - 1)];
+  return i < w.n && s >= 0 && s < a.numel ? s : -1;
+}
+__device__ __forceinline__ u32x4_t mask4(u32x4_t v, uint32_t keep) { return v & keep; }
+// Orders a wave's own LDS accesses (the hardware keeps them in order, the compiler has to).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// t[split][m][j] = sum over the split's k of A[a, j, k] x[m / top_k, k].  MT x RT tiles of 16 rows x 16 ranks.  A
+// wave takes 64 k of every row (a line) at a time, the four waves' turns lie side by side and their sums meet in LDS.
+//
+// Operands pass through a place in LDS of the wave's own, so that the main loop has no barrier: eight adjacent lanes load
+// a line of one row (straight to the operand's registers adjacent lanes lie in different rows, and a load takes 64 address
+// cycles in the place of 16), piece p of row i stands at p ^ (i & 7).  The next UN turns' loads are in flight while
+// these are multiplied.
+template <int MT, int RT, int UN>
+__global__ __launch_bounds__(256) void adapters_inner_kernel(AdapterArgs a) {
+  constexpr int ROWS = 16 * (MT + RT), LOADS = ROWS / 8;  // staged rows of a turn, loads of 8 rows
+  constexpr int STAGE = 4 * UN * ROWS * 128, RED = 3 * MT * RT * 1024;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+  __shared__ __attribute__((aligned(128))) uint8_t smem[STAGE > RED ? STAGE : RED];
+  const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
+  const RowTile w = row_tile(a, tile, 16 * MT);
+  int row_slot[2 * MT], slot[MT];
+#pragma unroll
+  for (int q = 0; q < 2 * MT; ++q) row_slot[q] = slot_of(a, w, q * 8 + (lane >> 3));
+#pragma unroll
+  for (int m = 0; m < MT; ++m) slot[m] = slot_of(a, w, m * 16 + l16);
+  if (w.adapter < 0) return;
+  const int rank = adapter_rank(a, w.adapter), r0 = blockIdx.y * kAdRankTile, piece = lane & 7;
   if (r0 >= rank && r0 > 0) return;
-  const uint16_t* xr[MT];
-  int slot[MT];
+  const uint16_t* p[LOADS];
+  uint32_t on[LOADS];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int i = m * 16 + l16;
-    const int s = i < n ? a.sorted[at + i] : -1;
-    slot[m] = s >= 0 && s < a.numel ? s : -1;
-    xr[m] = a.x + (int64_t)(max(slot[m], 0) / a.top_k) * a.ldx;  // (a padding entry's product is not stored)
+  for (int q = 0; q < LOADS; ++q) {
+    if (q < 2 * MT) {  // (a padding entry's product is not stored)
+      p[q] = a.x + (int64_t)(max(row_slot[q < 2 * MT ? q : 0], 0) / a.top_k) * a.ldx;
+      on[q] = ~0u;
+    } else {
+      const int j = r0 + (q - 2 * MT) * 8 + (lane >> 3);
+      p[q] = a.A + ((int64_t)w.adapter * a.r + (j < rank ? j : 0)) * a.K;
+      on[q] = j < rank ? ~0u : 0u;
+    }
   }
-  const uint16_t* ar[RT];
-  bool on[RT];
+  const int turns = (a.K + 255) >> 8;  // of the four waves
+  const int lo = (int)((int64_t)turns * split / a.splits), hi = (int)((int64_t)turns * (split + 1) / a.splits);
+  u32x4_t v[UN][LOADS];
+  auto load = [&](int turn) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    const int row = r0 + j * 16 + l16;
-    on[j] = row < rank;
-    ar[j] = a.A + ((int64_t)ad * a.r + (on[j] ? row : 0)) * a.K;
-  }
+    for (int u = 0; u < UN; ++u) {
+      const int k = (turn + u) * 256 + wv * 64 + piece * 8;
+      const bool in = turn + u < hi && k < a.K;  // (no branch around a load: what lies behind K is read elsewhere)
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) v[u][q] = mask4(*reinterpret_cast<const u32x4_t*>(p[q] + (in ? k : 0)), in ? on[q] : 0u);
+    }
+  };
   f32x4_t acc[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int steps = (a.K + 31) >> 5;
-  const int lo = (int)((int64_t)steps * blockIdx.y / a.splits), hi = (int)((int64_t)steps * (blockIdx.y + 1) / a.splits);
-  for (int s = lo + wv; s < hi; s += 4) {
-    const int k = s * 32 + g * 8;
-    const bool in = k < a.K;
-    uint4 xv[MT], av[RT];
+  uint8_t* stage = smem + wv * (UN * ROWS * 128);
+  uint8_t* mine = stage + (lane >> 3) * 128 + (piece ^ (lane >> 3)) * 16;
+  load(lo);
+  for (int turn = lo; turn < hi; turn += UN) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xv[m] = in ? *reinterpret_cast<const uint4*>(xr[m] + k) : zero4();
+    for (int u = 0; u < UN; ++u)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) av[j] = in && on[j] ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero4();
+      for (int q = 0; q < LOADS; ++q) *reinterpret_cast<u32x4_t*>(mine + (u * ROWS + q * 8) * 128) = v[u][q];
+    if (turn + UN < hi) load(turn + UN);
+    wave_lds_fence();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int u = 0; u < UN; ++u)
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av[j]),
-                                                            __builtin_bit_cast(bf16x8_t, xv[m]), acc[m][j], 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* at = stage + u * ROWS * 128 + l16 * 128 + ((4 * h + g) ^ (l16 & 7)) * 16;
+        bf16x8_t xf[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xf[m] = *reinterpret_cast<const bf16x8_t*>(at + m * 2048);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          const bf16x8_t af = *reinterpret_cast<const bf16x8_t*>(at + (MT + j) * 2048);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, xf[m], acc[m][j], 0, 0, 0);
+        }
+      }
+    wave_lds_fence();
   }
+  __syncthreads();
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(smem);
   if (wv > 0)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) red[wv - 1][m * RT + j][lane] = acc[m][j];
+      for (int j = 0; j < RT; ++j) red[((wv - 1) * MT * RT + m * RT + j) * 64 + lane] = acc[m][j];
   __syncthreads();
   if (wv > 0) return;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (slot[m] < 0) continue;
-    float* row = a.t + ((int64_t)blockIdx.y * a.numel + slot[m]) * a.r + r0;
+    float* row = a.t + ((int64_t)split * a.numel + slot[m]) * a.r + r0;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const f32x4_t v = (acc[m][j] + red[0][m * RT + j][lane]) + (red[1][m * RT + j][lane] + red[2][m * RT + j][lane]);
+      const f32x4_t* o = red + (m * RT + j) * 64 + lane;
+      const f32x4_t t = (acc[m][j] + o[0]) + (o[MT * RT * 64] + o[2 * MT * RT * 64]);
       const int c = j * 16 + g * 4;
-      if (r0 + c < a.r) *reinterpret_cast<f32x4_t*>(row + c) = v;
+      if (r0 + c < a.r) *reinterpret_cast<f32x4_t*>(row + c) = t;
     }
   }
 }
@@ -133,42 +188,97 @@ __device__ __forceinline__ void copy_rows(const AdapterArgs& a, int64_t first, i
   for (int64_t m = first; m < a.numel; m += step) {
     if (a.local[m] >= 0 && a.local[m] < a.L) continue;
     for (int c = threadIdx.x & 63; c < chunks; c += 64)
-      *reinterpret_cast<uint4*>(a.out + m * a.ldo + c * 8) = *reinterpret_cast<const uint4*>(a.base + m * a.ldb + c * 8);
+      *reinterpret_cast<u32x4_t*>(a.out + m * a.ldo + c * 8) = *reinterpret_cast<const u32x4_t*>(a.base + m * a.ldb + c * 8);
   }
 }
 
 // out[m, n] = base[m, n] + sum_j B[a, n, j] scale[a] t[m, j].  The tile's t stands in LDS as the matrix core takes it:
 // for each 16 rows and 16 ranks, lane groups 0 and 1 the upper halves of ranks 0..7 and 8..15, groups 2 and 3 the
-// lower ones.  A wave makes 64 columns at a time; the 16 rows of B of tile u are n = 16 (i / 4) + 4 u + i % 4, so that a
-// lane ends with 16 consecutive columns of one row.
-template <int MT>
-__global__ __launch_bounds__(256) void adapters_outer_kernel(AdapterArgs a) {
-  extern __shared__ uint16_t frag[];  // [MT][r / 16][64][8]
+// lower ones.  A wave makes 64 columns at a time.  Their columns of B (64 r values in a row, or 64 ranks of each at a time)
+// and the sums pass through places in LDS of the wave's own, so that all loads and stores are of whole lines by adjacent
+// lanes; the next columns' are in flight while these are made.  FR: 16-rank parts of t (r <= 16 FR).
+template <int MT, int FR>
+__global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, int strips) {
+  constexpr int RT = FR < 4 ? FR : 4;     // 16-rank parts that are staged at a time
+  constexpr int NL = 2 * RT;              // loads of them
+  constexpr bool LINES = RT == 4;         // staged rows of eight pieces (8 ranks each), piece p of row i at p ^ (i & 7);
+                                          // else of r / 8, as they lie in memory
+  constexpr int PITCH = 68;               // values between staged rows of sums
+  constexpr int FRAG = MT * FR * 1024, BS = 64 * RT * 32, SUMS = 16 * PITCH * 4;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
-  if ((int64_t)blockIdx.x >= a.row_blocks) {
-    const int64_t b = (int64_t)(blockIdx.x - a.row_blocks) * gridDim.y + blockIdx.y;
-    copy_rows(a, b * 4 + wv, (int64_t)(gridDim.x - a.row_blocks) * gridDim.y * 4);
+  __shared__ __attribute__((aligned(128))) uint8_t smem[FRAG + 4 * (BS + SUMS)];
+  const int first = (int)a.row_blocks * strips;
+  if ((int)blockIdx.x >= first) {
+    copy_rows(a, (int64_t)(blockIdx.x - first) * 4 + wv, (int64_t)(gridDim.x - first) * 4);
     return;
   }
-  int64_t at;
-  int n;
-  const int ad = row_tile(a, blockIdx.x, 16 * MT, at, n);
-  if (ad < 0) return;
-  const int rank = adapter_rank(a, ad), RK = (rank + 15) >> 4;
-  const float scale = a.scales ? a.scales[ad] : 1.0f;
-  for (int i = threadIdx.x; i < MT * RK * 32; i += 256) {  // eight ranks of one row
+  const int tile_row = blockIdx.x / strips, strip = blockIdx.x - tile_row * strips;
+  uint16_t* frag = reinterpret_cast<uint16_t*>(smem);  // [MT][parts][64][8]
+  uint8_t* bs = smem + FRAG + wv * (BS + SUMS);
+  float* sums = reinterpret_cast<float*>(bs + BS);
+  const RowTile w = row_tile(a, tile_row, 16 * MT);
+  int slot[MT][2];  // of the rows that this lane loads and stores
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) slot[m][h] = slot_of(a, w, m * 16 + h * 8 + (lane >> 3));
+  if (w.adapter < 0) return;
+  const int rank = adapter_rank(a, w.adapter), RK = (rank + 15) >> 4;
+  const float scale = a.scales ? a.scales[w.adapter] : 1.0f;
+  const uint16_t* Ba = a.B + (int64_t)w.adapter * a.N * a.r;
+  // the first columns of base and B
+  const int col = (lane & 7) * 8, pieces = a.r / 8;
+  u32x4_t base[MT][2], bv[NL];
+  // (No branches around loads, and none of them left out: columns behind N are read again and not stored.  The waits count
+  // what is in flight, and would else count on none of it.)
+  const uint32_t last_col = (uint32_t)a.N - 8, last_b = (uint32_t)a.N * (uint32_t)a.r - 8;
+  auto load_base = [&](int n0, int m, int h) __attribute__((always_inline)) {
+    base[m][h] = *reinterpret_cast<const u32x4_t*>(a.base + (int64_t)max(slot[m][h], 0) * a.ldb + min((uint32_t)(n0 + col), last_col));
+  };
+  auto load_b = [&](int n0, int c0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NL; ++q) {
+      const uint32_t i = q * 64 + lane;  // piece of the staged ones
+      uint32_t at;
+      if constexpr (LINES) {
+        const uint32_t row = i >> 3, j = c0 * 16 + ((i & 7) ^ (row & 7)) * 8;
+        at = min((uint32_t)n0 + row, (uint32_t)a.N - 1) * (uint32_t)a.r + (j < (uint32_t)a.r ? j : 0);
+      } else {
+        at = min((uint32_t)n0 * (uint32_t)a.r + i * 8, last_b);
+      }
+      bv[q] = *reinterpret_cast<const u32x4_t*>(Ba + at);
+    }
+  };
+  int n0 = (strip * 4 + wv) * 64;
+  load_b(n0, 0);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_base(n0, m, h);
+  // t: eight ranks of a row for each P adjacent threads, which share the splits
+  const int items = MT * RK * 32;
+  int P = 1;
+  while (P * 2 * items <= 256 && P < a.splits) P *= 2;
+  const int part = threadIdx.x & (P - 1);
+  for (int i = threadIdx.x / P; i < items; i += 256 / P) {
     const int l = i & 15, half = (i >> 4) & 1, tile = i >> 5, m = tile / RK, c = tile - m * RK;
-    const int pos = m * 16 + l, s = pos < n ? a.sorted[at + pos] : -1, j0 = c * 16 + half * 8;
+    const int s = slot_of(a, w, m * 16 + l), j0 = c * 16 + half * 8;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (s >= 0 && s < a.numel && j0 < a.r)
-      for (int p = 0; p < a.splits; ++p) {
-        const float4* q = reinterpret_cast<const float4*>(a.t + ((int64_t)p * a.numel + s) * a.r + j0);
-        const float4 u = q[0], w = q[1];
-        v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
-        v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+    if (s >= 0 && j0 < rank) {
+      const float* q = a.t + (int64_t)s * a.r + j0;
+#pragma unroll 4
+      for (int p = part; p < a.splits; p += P) {
+        const float4 x = *reinterpret_cast<const float4*>(q + (int64_t)p * a.numel * a.r);
+        const float4 y = *reinterpret_cast<const float4*>(q + (int64_t)p * a.numel * a.r + 4);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
       }
+    }
+    for (int d = P / 2; d >= 1; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += __shfl_xor(v[j], d);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -178,79 +288,80 @@ __global__ __launch_bounds__(256) void adapters_outer_kernel(AdapterArgs a) {
       lo[j] = pack_bf16x2(fabsf(dp) < INFINITY ? dp : 0.0f, fabsf(dq) < INFINITY ? dq : 0.0f);
     }
     uint16_t* d = frag + (int64_t)tile * 512 + (half * 16 + l) * 8;
-    *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(d + 256) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (part == 0) *reinterpret_cast<u32x4_t*>(d) = u32x4_t{hi[0], hi[1], hi[2], hi[3]};
+    if (part == P - 1) *reinterpret_cast<u32x4_t*>(d + 256) = u32x4_t{lo[0], lo[1], lo[2], lo[3]};
   }
   __syncthreads();
-  int slot[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int i = m * 16 + l16, s = i < n ? a.sorted[at + i] : -1;
-    slot[m] = s >= 0 && s < a.numel ? s : -1;
-  }
-  const uint16_t* Ba = a.B + (int64_t)ad * a.N * a.r;
-  for (int n0 = (blockIdx.y * 4 + wv) * 64; n0 < a.N; n0 += gridDim.y * 256) {
+  const int step = strips * 256;
+  for (; n0 < a.N; n0 += step) {
     f32x4_t acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int u = 0; u < 4; ++u) acc[m][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < RK; ++c) {
-      const int j0 = c * 16 + (g & 1) * 8;
-      uint4 bv[4];
+    for (int c0 = 0; c0 < (FR <= 4 ? 1 : RK); c0 += RT) {
+      if (c0) load_b(n0, c0);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int col = n0 + 16 * (l16 >> 2) + 4 * u + (l16 & 3);
-        bv[u] = zero4();
-        if (col < a.N && j0 < rank) {
-          bv[u] = *reinterpret_cast<const uint4*>(Ba + (int64_t)col * a.r + j0);
-          const int left = rank - j0;  // (values behind the adapter's own rank are not used)
-          if (left < 8) {
-            uint32_t w[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
+      for (int q = 0; q < NL; ++q)
+        if (LINES || q * 64 + lane < 64 * pieces) *reinterpret_cast<u32x4_t*>(bs + (q * 64 + lane) * 16) = bv[q];
+      if (FR <= 4 || c0 + RT >= RK) load_b(n0 + step, 0);
+      wave_lds_fence();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = 2 * j + 1 < left ? w[j] : (2 * j < left ? w[j] & 0xFFFFu : 0u);
-            bv[u] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+      for (int c = 0; c < RT; ++c) {
+        if (c0 + c >= RK) continue;
+        const int pc = 2 * c + (g & 1), left = rank - (c0 + c) * 16 - (g & 1) * 8;
+        uint32_t keep[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) keep[j] = 2 * j + 1 < left ? ~0u : (2 * j < left ? 0xFFFFu : 0u);
+        bf16x8_t bf[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = u * 16 + l16, at = LINES ? row * 8 + (pc ^ (row & 7)) : row * pieces + min(pc, pieces - 1);
+          const u32x4_t r = *reinterpret_cast<const u32x4_t*>(bs + at * 16);  // (values behind the adapter's own rank as 0)
+          bf[u] = __builtin_bit_cast(bf16x8_t, u32x4_t{r[0] & keep[0], r[1] & keep[1], r[2] & keep[2], r[3] & keep[3]});
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const bf16x8_t tv = *reinterpret_cast<const bf16x8_t*>(frag + ((int64_t)(m * RK + c0 + c) * 64 + lane) * 8);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) acc[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[u], tv, acc[m][u], 0, 0, 0);
         }
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const bf16x8_t tv = *reinterpret_cast<const bf16x8_t*>(frag + ((int64_t)(m * RK + c) * 64 + lane) * 8);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          acc[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, bv[u]), tv, acc[m][u], 0, 0, 0);
-      }
+      wave_lds_fence();
     }
-    const int col = n0 + 16 * g;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (slot[m] < 0) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) *reinterpret_cast<f32x4_t*>(sums + l16 * PITCH + u * 16 + g * 4) = acc[m][u];
+      wave_lds_fence();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (col + 8 * h >= a.N) continue;
-        const uint4 b = *reinterpret_cast<const uint4*>(a.base + (int64_t)slot[m] * a.ldb + col + 8 * h);
-        const f32x4_t p = acc[m][2 * h], q = acc[m][2 * h + 1];
-        *reinterpret_cast<uint4*>(a.out + (int64_t)slot[m] * a.ldo + col + 8 * h) =
-            make_uint4(pack_bf16x2(bf16_lo(b.x) + p[0], bf16_hi(b.x) + p[1]), pack_bf16x2(bf16_lo(b.y) + p[2], bf16_hi(b.y) + p[3]),
-                       pack_bf16x2(bf16_lo(b.z) + q[0], bf16_hi(b.z) + q[1]), pack_bf16x2(bf16_lo(b.w) + q[2], bf16_hi(b.w) + q[3]));
+        const float* o = sums + (h * 8 + (lane >> 3)) * PITCH + col;
+        const f32x4_t p = *reinterpret_cast<const f32x4_t*>(o), q = *reinterpret_cast<const f32x4_t*>(o + 4);
+        const u32x4_t b = base[m][h];
+        if (slot[m][h] >= 0 && n0 + col < a.N)
+          *reinterpret_cast<u32x4_t*>(a.out + (int64_t)slot[m][h] * a.ldo + n0 + col) =
+              u32x4_t{pack_bf16x2(bf16_lo(b[0]) + p[0], bf16_hi(b[0]) + p[1]), pack_bf16x2(bf16_lo(b[1]) + p[2], bf16_hi(b[1]) + p[3]),
+                         pack_bf16x2(bf16_lo(b[2]) + q[0], bf16_hi(b[2]) + q[1]), pack_bf16x2(bf16_lo(b[3]) + q[2], bf16_hi(b[3]) + q[3])};
+        load_base(n0 + step, m, h);
       }
+      wave_lds_fence();
     }
   }
 }
 
-// Rows of a workgroup's tile, row tiles of the batch (at most), and splits of K: about 512 workgroups, each with eight
-// steps of 32 k or more.
+// Rows of a workgroup's tile, row tiles of the batch (at most), and splits of K: about 512 workgroups, each with a turn
+// of its four waves (256 k) or more.
 static int adapter_rows(int block_m) { return block_m <= 16 ? 16 : block_m <= 32 ? 32 : 64; }
 static int64_t adapter_row_blocks(int64_t numel, int L, int block_m, int* per) {
-  const int64_t blocks = (numel + std::min<int64_t>(L, numel) * (block_m - 1)) / block_m +
-                         ((numel + std::min<int64_t>(L, numel) * (block_m - 1)) % block_m != 0);
+  const int64_t rows = numel + std::min<int64_t>(L, numel) * (block_m - 1);
   *per = (block_m + adapter_rows(block_m) - 1) / adapter_rows(block_m);
-  return blocks * *per;
+  return (rows + block_m - 1) / block_m * *per;
 }
 static int adapter_splits(int64_t row_blocks, int r, int K) {
   const int64_t groups = std::max<int64_t>(1, row_blocks * ((r + kAdRankTile - 1) / kAdRankTile));
-  const int64_t by_k = std::max(1, (K + 31) / 32 / 8);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / groups, by_k, kAdMaxSplits}));
+  const int64_t by_k = (K + 255) / 256;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kAdGroups / groups, by_k, kAdMaxSplits}));
 }
 
 static int adapter_sizes(const char* fn, int64_t numel, int32_t L, int32_t r, int32_t N, int32_t K, int32_t block_m) {
@@ -258,21 +369,29 @@ static int adapter_sizes(const char* fn, int64_t numel, int32_t L, int32_t r, in
               "%s: numel=%lld L=%d r=%d N=%d K=%d block_m=%d", fn, (long long)numel, L, r, N, K, block_m);
   MOE_REQUIRE(r % 8 == 0 && r <= kAdMaxRank && N % 8 == 0 && K % 8 == 0, MOE_EUNSUPPORTED,
               "%s: r=%d (at most %d), N=%d and K=%d must be multiples of 8", fn, r, kAdMaxRank, N, K);
+  MOE_REQUIRE((int64_t)N * r < (1ll << 30), MOE_EUNSUPPORTED, "%s: N=%d r=%d: an adapter of 2^30 values or more", fn, N, r);
   MOE_REQUIRE(L <= kAdMaxAdapters, MOE_EUNSUPPORTED, "%s: %d adapters (at most %d)", fn, L, kAdMaxAdapters);
   MOE_REQUIRE(numel < (1ll << 31) - 256 * kAdMaxAdapters, MOE_EUNSUPPORTED, "%s: numel=%lld too large", fn, (long long)numel);
   return MOE_OK;
 }
 
+template <int MT, int RT, int FR, int UN>
+static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st) {
+  // (splits and strips of a row tile side by side: what runs at once then takes whole rows.  One slice of every row at a
+  // time, 1 KB in 8, left most memory channels idle)
+  const dim3 gi((unsigned)(a.row_blocks * a.splits), (unsigned)((a.r + kAdRankTile - 1) / kAdRankTile));
+  hipLaunchKernelGGL((adapters_inner_kernel<MT, RT, UN>), gi, dim3(256), 0, st, a);
+  const int64_t strips = std::max<int64_t>(1, std::min<int64_t>((a.N + 255) / 256, (kAdStrips + a.row_blocks - 1) / a.row_blocks));
+  hipLaunchKernelGGL((adapters_outer_kernel<MT, FR>), dim3((unsigned)(a.row_blocks * strips + copies)), dim3(256), 0, st, a,
+                     (int)strips);
+}
 template <int MT>
 static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st) {
-  const dim3 gi((unsigned)a.row_blocks, (unsigned)a.splits, (unsigned)((a.r + kAdRankTile - 1) / kAdRankTile));
-  if (a.r <= 16) hipLaunchKernelGGL((adapters_inner_kernel<MT, 1>), gi, dim3(256), 0, st, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((adapters_inner_kernel<MT, 2>), gi, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((adapters_inner_kernel<MT, 4>), gi, dim3(256), 0, st, a);
-  const int64_t strips = (a.N + 255) / 256;
-  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(strips, (1024 + a.row_blocks - 1) / a.row_blocks));
-  hipLaunchKernelGGL((adapters_outer_kernel<MT>), dim3((unsigned)(a.row_blocks + copies), (unsigned)y), dim3(256),
-                     (size_t)MT * ((a.r + 15) / 16) * 1024, st, a);
+  constexpr int UN = MT == 1 ? 2 : 1;
+  if (a.r <= 16) launch_adapters<MT, 1, 1, UN>(a, copies, st);
+  else if (a.r <= 32) launch_adapters<MT, 2, 2, UN>(a, copies, st);
+  else if (a.r <= 64) launch_adapters<MT, 4, 4, UN>(a, copies, st);
+  else launch_adapters<MT, 4, 16, UN>(a, copies, st);
 }
 
 }  // namespace moe
@@ -328,7 +447,7 @@ extern "C" int moe_adapters_add(const uint16_t* base, int64_t ld_base, const uin
               (long long)work_elems, (long long)(a.splits * numel * r));
   MOE_REQUIRE(a.row_blocks < (1ll << 22) / ((r + kAdRankTile - 1) / kAdRankTile), MOE_EUNSUPPORTED,
               "moe_adapters_add: %lld row tiles", (long long)a.row_blocks);
-  const int64_t copies = in_place ? 0 : std::min<int64_t>((numel + 3) / 4, 256);
+  const int64_t copies = in_place ? 0 : std::min<int64_t>((numel + 3) / 4, 512);
   const int rows = adapter_rows(block_m);
   if (rows == 16) launch_adapters<1>(a, copies, stream);
   else if (rows == 32) launch_adapters<2>(a, copies, stream);
