@@ -8,6 +8,7 @@ every computation runs in libmoe_w4a16 on the current stream of the tensors' dev
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -36,6 +37,7 @@ class Routing(NamedTuple):
     balance: torch.Tensor
 
 
+@functools.lru_cache(maxsize=256)
 def router_workspace(M: int, E: int) -> int:
     """Bytes of the workspace of moe_router's statistics."""
     n = C.c_int64()
@@ -160,9 +162,20 @@ def moe_router_grad(logits: torch.Tensor, topk_ids: torch.Tensor, d_weights: Opt
     return out
 
 
+def _once(backward):
+    """once_differentiable, without its time (5 us a call) where no second derivative can be asked for."""
+    guarded = torch.autograd.function.once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return call
+
+
 class _ExpertsRouter(torch.autograd.Function):
+    # (`aside` takes the outputs without a gradient: each output of the function costs the graph's bookkeeping 5 us)
     @staticmethod
-    def forward(ctx, logits, bias, live, top_k, kind, renormalise, scale):
+    def forward(ctx, logits, bias, live, top_k, kind, renormalise, scale, means_grad, aside):
         (M, E), dev = logits.shape, logits.device
         ids, weights = _new_outputs(M, E, top_k, dev)
         counts, means, balance, tokens = stats = _new_stats(E, dev)
@@ -170,28 +183,32 @@ class _ExpertsRouter(torch.autograd.Function):
         _router(logits, top_k, kind, bias, live, renormalise, scale, ids, weights, stats, work)
         ctx.save_for_backward(logits, live, ids, counts, tokens)
         ctx.how = (kind, top_k, renormalise, scale)
-        ctx.mark_non_differentiable(ids, counts)
         ctx.set_materialize_grads(False)
-        return ids, weights, counts, means, balance.view(())
+        aside += (ids, counts, means)
+        balance = balance.view(())
+        return (weights, balance, means) if means_grad else (weights, balance)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, _ids, d_weights, _counts, d_means, d_balance):
+    @_once
+    def backward(ctx, d_weights, d_balance, d_means=None):
         logits, live, ids, counts, tokens = ctx.saved_tensors
         kind, top_k, renormalise, scale = ctx.how
         out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        c = lambda t: None if t is None else t.contiguous()  # noqa: E731  (gradients may arrive broadcast)
-        _router_grad(logits, live, kind, top_k, renormalise, scale, ids, c(d_weights), counts, tokens, c(d_means),
-                     c(d_balance), out)
-        return out, None, None, None, None, None, None
+        if d_weights is not None and not d_weights.is_contiguous():   # (gradients may arrive broadcast)
+            d_weights = d_weights.contiguous()
+        if d_means is not None:
+            d_means = d_means.contiguous()
+        _router_grad(logits, live, kind, top_k, renormalise, scale, ids, d_weights, counts, tokens, d_means, d_balance, out)
+        return out, None, None, None, None, None, None, None, None
 
 
 def moe_experts_router(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
-                       renormalise: bool = False, scale: float = 1.0, live: Optional[torch.Tensor] = None) -> Routing:
+                       renormalise: bool = False, scale: float = 1.0, live: Optional[torch.Tensor] = None,
+                       means_grad: bool = False) -> Routing:
     """Differentiable moe_router with the batch's statistics: Routing(ids, weights, counts, means, balance).
 
-    The gradients of weights, means and balance reach the logits in one pass; they have the logits' type and are
-    once differentiable.  The choice, the counts and the selection bias have no gradient.  balance is
+    The gradients of weights and balance, and with `means_grad` of means, reach the logits in one pass; they have the
+    logits' type and are once differentiable.  The choice, the counts and the selection bias have no gradient.  balance is
     E * sum_e (counts_e / sum counts) * means_e; for counts that are summed over several ranks' batches form the same
     sum from `means` (the ranks' mean of it is the loss of the whole batch when they hold equally many tokens).
 
@@ -201,9 +218,13 @@ def moe_experts_router(logits: torch.Tensor, top_k: int, score: str = "softmax",
     _check_logits(logits, top_k, bias, live)
     if not 1 <= top_k <= logits.shape[1]:
         raise ValueError(f"top_k={top_k} of {logits.shape[1]} experts")
-    return Routing(*_ExpertsRouter.apply(logits, bias, live, top_k, kind, renormalise, scale))
+    aside = []
+    out = _ExpertsRouter.apply(logits, bias, live, top_k, kind, renormalise, scale, means_grad, aside)
+    ids, counts, means = aside
+    return Routing(ids, out[0], counts, out[2] if means_grad else means, out[1])
 
 
+@functools.lru_cache(maxsize=256)
 def combine_grad_workspace(M: int, H: int) -> int:
     """float32 values of the workspace of moe_combine_grad's norm weight gradient."""
     n = C.c_int64()
@@ -270,7 +291,7 @@ class _ExpertsCombine(torch.autograd.Function):
         return out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, grad):
         y, weights, norm_w, local = ctx.saved_tensors
         # (a gradient may arrive broadcast or transposed, or with rows that 16-byte loads cannot take)

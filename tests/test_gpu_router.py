@@ -221,7 +221,7 @@ def test_differentiable_form():
     M, E, k = 50, 96, 4
     lg = U.logits(M, E, BF, 6).cuda().requires_grad_(True)
     bias = torch.from_numpy(0.1 * r.standard_normal(E).astype(np.float32)).cuda()
-    rt = P.moe_experts_router(lg, k, score="sigmoid", bias=bias, renormalise=True, scale=2.0)
+    rt = P.moe_experts_router(lg, k, score="sigmoid", bias=bias, renormalise=True, scale=2.0, means_grad=True)
     ids, w, st = P.moe_router(lg.detach(), k, score="sigmoid", bias=bias, renormalise=True, scale=2.0, stats=True)
     assert torch.equal(rt.ids, ids) and torch.equal(rt.weights, w) and torch.equal(rt.counts, st.counts)
     assert torch.equal(rt.means, st.means) and torch.equal(rt.balance, st.balance[0]) and rt.balance.dim() == 0
@@ -238,6 +238,13 @@ def test_differentiable_form():
                        P.moe_router_grad(lg.detach(), ids, dw, stats=st, d_balance=one(0.5), **how))
     broadcast = grads(rt.weights.sum())           # a gradient that arrives with stride 0
     assert torch.equal(broadcast, P.moe_router_grad(lg.detach(), ids, torch.ones_like(w), **how))
+    plain = P.moe_experts_router(lg, k, score="sigmoid", bias=bias, renormalise=True, scale=2.0)
+    assert not plain.means.requires_grad and torch.equal(plain.means, rt.means) and torch.equal(plain.weights, rt.weights)
+    assert torch.equal(torch.autograd.grad((plain.weights, plain.balance), lg, (dw, torch.full((), 0.5, device="cuda")))[0],
+                       P.moe_router_grad(lg.detach(), ids, dw, stats=st, d_balance=one(0.5), **how))
+    twice = torch.autograd.grad(P.moe_experts_router(lg, k).weights.pow(2).sum(), lg, create_graph=True)[0]
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        twice.sum().backward()
     with pytest.raises(ValueError, match="top_k"):
         P.moe_experts_router(lg, E + 1)
     empty = P.moe_experts_router(torch.empty((0, E), dtype=BF, device="cuda", requires_grad=True), k)
