@@ -193,10 +193,16 @@ __device__ __forceinline__ float sigmoid_shifted(float x, float shift) {
 template <int LANES, int V>
 __device__ __forceinline__ float row_shares(const float (&x)[V], int sigmoid, float m, float (&u)[V]) {
   float total = 0.0f;
-  if (sigmoid) {
+  if (sigmoid && __any(m < 0.0f)) {
     const float shift = fminf(m, 0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) u[j] = sigmoid_shifted(x[j], shift);
+  } else if (sigmoid) {  // (the same values with one exponential)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float z = exp_neg(-fabsf(x[j]));
+      u[j] = (x[j] >= 0.0f ? 1.0f : z) * __builtin_amdgcn_rcpf(1.0f + z);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) u[j] = exp_neg(x[j] - m);
@@ -210,21 +216,15 @@ __device__ __forceinline__ float row_shares(const float (&x)[V], int sigmoid, fl
 }
 
 // The row's largest logit (0 for a row of -inf), and whether its weights are NaN: a NaN, or an infinite logit under a
-// softmax.  (As integers: positive values rise with their bits, and only NaNs lie beyond the infinities.)
+// softmax.  (The maximum that hands a NaN on: one instruction for two logits and both answers.)
 template <int LANES, int V>
 __device__ __forceinline__ float row_max(const float (&x)[V], int sigmoid, int grp, bool& bad) {
-  float m = -INFINITY;
-  int up = 0;
-  uint32_t down = 0;
+  float m = x[0];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    m = fmaxf(m, x[j]);
-    up = max(up, __float_as_int(x[j]));
-    down = max(down, __float_as_uint(x[j]));
-  }
-  bad = group_any<LANES>(up > (sigmoid ? 0x7F800000 : 0x7F7FFFFF) || down > 0xFF800000u, grp);
-  m = group_max<LANES>(m);
-  return m == -INFINITY ? 0.0f : m;
+  for (int j = 1; j < V; ++j) m = __builtin_elementwise_maximum(m, x[j]);
+  bad = group_any<LANES>(m != m || (!sigmoid && m == INFINITY), grp);
+  m = group_max<LANES>(m);  // (passes a lane's NaN over)
+  return m > -INFINITY ? m : 0.0f;
 }
 
 // Falling order by odd-even merging (comparators that are known at compile time; V need not be a power of two).
@@ -296,12 +296,11 @@ __device__ __forceinline__ uint32_t nine_largest(uint32_t (&key)[V], int sub) {
   return sub < 8 ? r : (sub == 8 ? left : 0);
 }
 
-// A biased score in fp32 (off by less than 2^-20 and half a step of the sum).
+// A biased score in fp32 (a sigmoid's exponential may overflow: the score is then 0).
 __device__ __forceinline__ float biased(float x, float b, int sigmoid, float m, float inv) {
   constexpr float kL = 0x1.715476p+0f;
-  const float z = __builtin_amdgcn_exp2f((sigmoid ? -fabsf(x) : x - m) * kL);
-  const float s = sigmoid ? (x >= 0.0f ? 1.0f : z) * __builtin_amdgcn_rcpf(1.0f + z) : z * inv;
-  return s + b;
+  if (sigmoid) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kL)) + b;
+  return fmaf(__builtin_amdgcn_exp2f((x - m) * kL), inv, b);
 }
 
 // exp in 64 bits, to a few units in the last place: exp(x) = 2^n exp(r), |r| <= ln(2) / 2, by the series of exp(r)
@@ -385,7 +384,7 @@ template <int IB, bool BIAS>
 struct Cut {
   static constexpr float kTop = (float)((1u << (32 - IB)) - 256), kStep = kTop / (BIAS ? 2.0f : 32.0f);
   static __device__ __forceinline__ uint32_t key(float v, float off, int index) {
-    const uint32_t q = (uint32_t)fminf(fmaxf(fmaf(v, kStep, off), 1.0f), (float)((1u << (32 - IB)) - 1));
+    const uint32_t q = (uint32_t)__builtin_amdgcn_fmed3f(fmaf(v, kStep, off), 1.0f, (float)((1u << (32 - IB)) - 1));
     const uint32_t keep = v > -INFINITY ? ~0u : 0u;  // (a mask: a choice of the whole would become a branch)
     return ((q << IB) | (uint32_t)index) & keep;
   }
@@ -431,7 +430,7 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
     float x[V], b[V];
     load_logits<T, LANES, V>(row, sub, a.E, wide & 1, reinterpret_cast<float*>(lkeys[wv]), lane, x);
     const bool live = in && mark >= 0;
-    mask_logits<LANES, V>(sub, live ? a.E : 0, x);
+    if (a.E < LANES * V || __any(!live)) mask_logits<LANES, V>(sub, live ? a.E : 0, x);
     if constexpr (BIAS) load_logits<float, LANES, V>(a.bias, sub, a.E, wide & 4, reinterpret_cast<float*>(lkeys[wv]), lane, b);
     bool bad;
     const float m = row_max<LANES, V>(x, a.sigmoid, grp, bad);
@@ -468,7 +467,7 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
           }
           top = group_max<LANES>(top);
           // A sigmoid is off by less than 5 * 2^-24 (its exponential by |x| 1.5 * 2^-24 and a unit, of which at most
-          // 1.1 * 2^-24 remains, the sum, the reciprocal and the product by a unit and halves), 2.5 steps of 2^-23; the sum
+          // 1.1 * 2^-24 remains, the sum and the reciprocal by a unit each), 2.5 steps of 2^-23; the sum
           // with the bias by half a step for each unit of `top`, the cut by two.  A softmax's row sum adds less
           // than 26 * 2^-24 that all scores share.
           tol = (a.sigmoid ? 12 : 28) + (int)fminf(2.0f * fabsf(top), 1e6f);
@@ -706,7 +705,7 @@ __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradArgs a, int 
   const bool live = in && mark >= 0;
   if (!live || sub >= a.k || id >= a.E) id = -1;
   const float xj = id >= 0 ? load_logit(row + id) : -INFINITY;
-  mask_logits<LANES, V>(sub, live ? a.E : 0, x);
+  if (a.E < LANES * V || __any(!live)) mask_logits<LANES, V>(sub, live ? a.E : 0, x);
   bool bad;
   const float m = row_max<LANES, V>(x, a.sigmoid, grp, bad);
   float q[V], total = 0.0f, aq = 0.0f;
@@ -756,7 +755,10 @@ __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradArgs a, int 
     float v = chosen[wv][j][lane];
     if (dense) {
       float g = coef[j] - aq;
-      if (a.sigmoid) g *= sigmoid_shifted(-fmaxf(x[j], -104.0f), 0.0f);
+      if (a.sigmoid) {
+        const float z = exp_neg(-fabsf(x[j]));
+        g *= (x[j] >= 0.0f ? z : 1.0f) * __builtin_amdgcn_rcpf(1.0f + z);
+      }
       v = fmaf(q[j], g - rest, v);
     }
     out[j] = bad ? NAN : v;
