@@ -11,6 +11,7 @@ block_m: the least of 16, 32 and 64 that holds an adapter's mean number of rows,
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import Optional
 
 import torch
@@ -19,6 +20,7 @@ from . import _lib as L
 from .experts import _BF16, _F32, _I32, _call, _check, _check_align, _ld, _live_ptr
 
 
+@functools.lru_cache(maxsize=256)
 def adapters_workspace(numel: int, n_adapters: int, rank: int, K: int, block_m: int) -> int:
     """float32 values of moe_adapters_add's workspace for numel rows."""
     n = C.c_int64()
