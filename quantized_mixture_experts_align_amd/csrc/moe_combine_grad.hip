@@ -17,6 +17,7 @@ namespace moe {
 constexpr int kCgThreads = 256;
 constexpr int kCgMaxTopK = 16;
 constexpr int kCgParts = 512;      // workgroups that leave partial sums of dn, at most
+constexpr int kCgGrid = 1 << 20;    // workgroups at most (2^32 threads are a launch's limit); they stay for more tokens
 constexpr int kCgMaxNormH = 12288; // columns whose dn a workgroup can hold in LDS
 
 struct CombineGradArgs {
@@ -404,7 +405,7 @@ extern "C" int moe_combine_grad(const uint16_t* y, const float* topk_weights, co
   const CombineGradArgs a{y, topk_weights, slot_local_ids, norm_w, eps, routed_scaling_factor, M, top_k, H, d_out, ld_dout,
                           dy, d_weights, d_norm_w ? work : nullptr};
   if (M > 0) {
-    const unsigned grid = (unsigned)(d_norm_w ? parts : M);
+    const unsigned grid = (unsigned)(d_norm_w ? parts : std::min<int64_t>(M, kCgGrid));
     const size_t lds = d_norm_w ? (size_t)H * 4 : 0;
     const int chunks = H / 8;
     if (top_k <= 8 && chunks <= 1024) {  // (what two chunks a thread and eight slots hold in registers)

@@ -321,12 +321,10 @@ __device__ __forceinline__ double exp_wide(double x) {
 
 // The 64-bit key of an expert (0: not eligible): its logit with the index behind it, or its biased score in 64 bits
 // whose lowest 10 places give way to the index.
-template <typename T>
-__device__ __forceinline__ uint64_t wide_key(const T* row, const float* bias, int e, int sigmoid, float m, double total) {
-  const float x = load_logit(row + e);
+template <bool BIAS>
+__device__ __forceinline__ uint64_t wide_key(float x, float b, int e, int sigmoid, float m, double total) {
   if (!(x > -INFINITY)) return 0;
-  if (!bias) return ((uint64_t)sortable(x) << 32) | (uint32_t)(1023 - e);
-  const float b = bias[e];
+  if (!BIAS) return ((uint64_t)sortable(x) << 32) | (uint32_t)(1023 - e);
   if (!(b > -INFINITY)) return 0;
   const double z = exp_wide(sigmoid ? -(double)x : (double)x - (double)m);
   const double s = sigmoid ? 1.0 / (1.0 + z) : z / total;
@@ -347,15 +345,17 @@ __device__ __forceinline__ double wide_total(const T* row, int E, int sub, float
 }
 // The selection over 64-bit keys of all experts, for top_k > 8 and rows with more candidates than lanes: it reads the
 // row again and keeps its keys in LDS ([V][64] of the wave).  E = 0: none.
-template <typename T, int LANES, int V>
+template <typename T, int LANES, int V, bool BIAS>
 __device__ __forceinline__ int select_wide(const T* row, const float* bias, int E, int k, int sigmoid, int lane, float m,
                                            uint64_t* keys) {
   const int sub = lane & (LANES - 1);
-  const double total = bias && !sigmoid ? wide_total<T, LANES, V>(row, E, sub, m) : 1.0;
+  const double total = BIAS && !sigmoid ? wide_total<T, LANES, V>(row, E, sub, m) : 1.0;
 #pragma unroll 1
   for (int j = 0; j < V; ++j) {
     const int e = expert_of<LANES>(sub, j);
-    keys[j * 64 + lane] = e < E ? wide_key(row, bias, e, sigmoid, m, total) : 0;  // (a lane reads its own alone)
+    uint64_t key = 0;
+    if (e < E) key = wide_key<BIAS>(load_logit(row + e), BIAS ? bias[e] : 0.0f, e, sigmoid, m, total);
+    keys[j * 64 + lane] = key;  // (a lane reads its own alone)
   }
   int mine = -1;
   uint64_t last = ~0ull;
@@ -390,10 +390,12 @@ struct Cut {
   }
 };
 
-// LDS of a wave for the candidates of a near tie: their number in each group, experts and 64-bit keys, and the choice.
+// LDS of a wave for the candidates of a near tie: their number in each group, experts, logits, biases and 64-bit keys,
+// and the choice.
 struct NearTie {
   int32_t n[4];
   int32_t expert[64];
+  float logit[64], bias[64];
   uint64_t key[64];
   int32_t choice[64];
 };
@@ -512,11 +514,15 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
 #pragma unroll 4
           for (int j = 0; j < V; ++j) {
             const int c = expert_of<LANES>(sub, j);
-            float y = stash[j * 64];
-            if constexpr (BIAS) y = y > -INFINITY ? biased(y, stash[(V + j) * 64], a.sigmoid, m, inv) : y;
-            if (Cut<IB, BIAS>::key(y, off, LAST - c) >= least) {
+            const float y = stash[j * 64], z = BIAS ? stash[(V + j) * 64] : 0.0f;
+            const float v = BIAS && y > -INFINITY ? biased(y, z, a.sigmoid, m, inv) : y;
+            if (Cut<IB, BIAS>::key(v, off, LAST - c) >= least) {
               const int at = atomicAdd(&lt.n[grp], 1);
-              if (at < LANES) lt.expert[grp * LANES + at] = c;
+              if (at < LANES) {
+                lt.expert[grp * LANES + at] = c;
+                lt.logit[grp * LANES + at] = y;
+                lt.bias[grp * LANES + at] = z;
+              }
             }
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -525,22 +531,27 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
           else {
             const double sum = BIAS && !a.sigmoid ? wide_total<T, LANES, V>(row, live ? a.E : 0, sub, m) : 1.0;
             const int c = sub < n ? lt.expert[lane] : 0;
-            const uint64_t mykey = sub < n ? wide_key(row, a.bias, c, a.sigmoid, m, sum) : 0;
+            const float y = sub < n ? lt.logit[lane] : -INFINITY;
+            const uint64_t mykey = wide_key<BIAS>(y, lt.bias[lane], c, a.sigmoid, m, sum);
             lt.key[lane] = mykey;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             int rank = 0;
 #pragma unroll
             for (int i = 0; i < LANES; ++i) rank += lt.key[grp * LANES + i] > mykey;
-            if (sub < n && rank < a.k) lt.choice[grp * LANES + rank] = c;
+            const bool chosen = mykey && rank < a.k;
+            if (chosen) lt.choice[grp * LANES + rank] = c;
+            xj = -INFINITY;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             mine = lt.choice[lane];
-            xj = mine >= 0 ? load_logit(row + mine) : -INFINITY;
+            int ps, pj;
+            place_of<LANES>(max(mine, 0), ps, pj);
+            if (mine >= 0) xj = stash[pj * 64 + ps - sub];
           }
         }
       }
     }
     if (wide_keys) {
-      mine = select_wide<T, LANES, V>(row, BIAS ? a.bias : nullptr, live ? a.E : 0, a.k, a.sigmoid, lane, m, lkeys[wv]);
+      mine = select_wide<T, LANES, V, BIAS>(row, a.bias, live ? a.E : 0, a.k, a.sigmoid, lane, m, lkeys[wv]);
       xj = mine >= 0 ? load_logit(row + mine) : -INFINITY;
     }
     const bool has = mine >= 0;

@@ -154,6 +154,44 @@ def test_replayed_graph():
         assert all(torch.equal(a, b) for a, b in zip(out, want)), turn
 
 
+def test_captured_forward_and_backward_of_the_differentiable_form():
+    M, k, H = 40, 2, 256
+    sets = [inputs(M, k, H, s, dead=0.0) for s in (1, 2, 3)]
+    local = sets[0][2].cuda()
+    leaves = [sets[0][i].cuda().requires_grad_(True) for i in (0, 1, 4)]
+    dout = sets[0][3].cuda()
+
+    def step(a):
+        o = P.moe_experts_combine(a[0], a[1], local, norm_w=a[2], eps=EPS)
+        return (o, *torch.autograd.grad(o, a, dout))
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(leaves)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(leaves)
+    for turn in range(4):
+        s = sets[turn % 3]
+        with torch.no_grad():
+            for leaf, i in zip(leaves, (0, 1, 4)):
+                leaf.copy_(s[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step([s[i].cuda().requires_grad_(True) for i in (0, 1, 4)])
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), turn
+        del want
+
+
+def test_more_tokens_than_workgroups():
+    M, H = (1 << 20) + 777, 8
+    y, g, local, dout, _ = inputs(M, 1, H, 77, dead=0.1)
+    got = P.moe_combine_grad(y.cuda(), g.cuda(), local.cuda(), dout.cuda())
+    check(y, g, local, dout, None, 1.0, got, "many")
+
+
 def test_refusals_of_the_wrappers():
     y, g, local, dout, n = (t.cuda() for t in inputs(4, 2, 64, 1))
     for call, text in ((lambda: P.moe_combine_grad(y[:7], g, local, dout), "must have a row"),

@@ -110,6 +110,46 @@ def test_biased_scores_that_differ_in_the_tenth_place(score):
     assert (got.cpu().numpy() == U.choose64(l.astype(np.float64), score, bias, k, None)).all()
 
 
+def near_ties(M, E, top, score, biased, seed):
+    """Logits (fp32) and biases whose `top` best experts of a row lie within a few 2^-24 of each other (their order is
+    another in every row), the others well below."""
+    r = np.random.default_rng([seed, E])
+    close = r.permutation(top) * 1.0
+    order = np.stack([r.permutation(E) for _ in range(M)])
+    l = np.full((M, E), -6.0) + 0.5 * r.standard_normal((M, E))
+    bias = (0.05 * r.random(E)).astype(np.float32) if biased else None
+    for t in range(M):
+        e = order[t, :top]
+        delta = r.permutation(close) * 2.0 ** -23
+        if not biased:
+            l[t, e] = 2.0 + delta
+        elif score == "sigmoid":
+            s = 0.8 - bias[e] + delta
+            l[t, e] = np.log(s / (1.0 - s))
+        else:                                      # probabilities of about 0.6 / top, what is left for the others
+            p = 0.6 / top * (1.05 - bias[e]) + delta
+            l[t, e] = np.log(p)
+            rest = np.setdiff1d(np.arange(E), e)
+            l[t, rest] += np.log((1.0 - p.sum()) / np.exp(l[t, rest]).sum())
+    if biased and score == "softmax":
+        bias = (bias * np.float32(0.6 / top)).astype(np.float32)
+    return l.astype(np.float32), bias
+
+
+@pytest.mark.parametrize("E,top,k", [(24, 6, 4), (64, 12, 8), (129, 5, 3), (256, 14, 8), (512, 12, 7), (1000, 30, 8), (256, 40, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_near_ties_are_ordered_exactly(E, top, k, score, biased):
+    """A few candidates of a row closer than fp32 keys tell apart, and more of them than a group has lanes."""
+    l, bias = near_ties(37, E, top, score, biased, k)
+    got = P.moe_router(torch.from_numpy(l).cuda(), k, score=score, renormalise=True,
+                       bias=None if bias is None else torch.from_numpy(bias).cuda())
+    want = U.choose64(l.astype(np.float64), score, bias, k, None)
+    assert (got[0].cpu().numpy() == want).all()
+    w = U.router64(l.astype(np.float64), score, want, True, 1.0, None)[0]
+    assert_close(got[1], w, U.router_error(l, E) * w, "weights")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("at", [-1e30, -3e4, -150.0, 80.0, 1e30])
 def test_logits_far_from_zero(score, at):
@@ -292,6 +332,35 @@ def test_replayed_graphs_and_two_streams():
             step(*want)
             for got, ref in zip((*b[:3], *b[3], b[5]), (*want[:3], *want[3], want[5])):
                 assert torch.equal(got, ref), (turn, i)
+
+
+def test_captured_forward_and_backward_of_the_differentiable_form():
+    M, E, k = 96, 64, 4
+    data = [U.logits(M, E, F32, s).cuda() for s in range(4)]
+    leaf = data[0].clone().requires_grad_(True)
+    dw, share = torch.ones((M, k), device="cuda"), torch.full((), 0.1, device="cuda")
+    how = dict(score="sigmoid", renormalise=True)
+
+    def step(x):
+        rt = P.moe_experts_router(x, k, **how)
+        return rt.ids, rt.weights, rt.counts, rt.balance, torch.autograd.grad((rt.weights, rt.balance), x, (dw, share))[0]
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                  # (a first pass outside, whose graph is gone before the capture)
+        step(leaf)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(leaf)
+    for turn in range(4):
+        with torch.no_grad():
+            leaf.copy_(data[turn])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(data[turn].clone().requires_grad_(True))
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), turn
+        del want
 
 
 def test_refusals_of_the_wrappers():
