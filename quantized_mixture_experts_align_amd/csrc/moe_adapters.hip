@@ -69,7 +69,6 @@ __device__ __forceinline__ int slot_of(const AdapterArgs& a, const RowTile& w, i
   const int s = a.sorted[w.at + min(i, w.n - 1)];
   return i < w.n && s >= 0 && s < a.numel ? s : -1;
 }
-__device__ __forceinline__ u32x4_t mask4(u32x4_t v, uint32_t keep) { return v & keep; }
 // Orders a wave's own LDS accesses (the hardware keeps them in order, the compiler has to).
 __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -82,9 +81,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 // Operands pass through a place in LDS of the wave's own, so that the main loop has no barrier: eight adjacent lanes load
 // a line of one row (straight to the operand's registers adjacent lanes lie in different rows, and a load takes 64 address
 // cycles in the place of 16), piece p of row i stands at p ^ (i & 7).  The next UN turns' loads are in flight while
-// these are multiplied.
+// these are multiplied (two such sets took no less time, and beside 64 sums they spill).
 template <int MT, int RT, int UN>
-__global__ __launch_bounds__(256) void adapters_inner_kernel(AdapterArgs a) {
+__global__ __launch_bounds__(256, 2) void adapters_inner_kernel(AdapterArgs a) {
   constexpr int ROWS = 16 * (MT + RT), LOADS = ROWS / 8;  // staged rows of a turn, loads of 8 rows
   constexpr int STAGE = 4 * UN * ROWS * 128, RED = 3 * MT * RT * 1024;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
@@ -97,20 +96,19 @@ __global__ __launch_bounds__(256) void adapters_inner_kernel(AdapterArgs a) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) slot[m] = slot_of(a, w, m * 16 + l16);
   if (w.adapter < 0) return;
-  const int rank = adapter_rank(a, w.adapter), r0 = blockIdx.y * kAdRankTile, piece = lane & 7;
+  const int rank = adapter_rank(a, w.adapter), r0 = (int)blockIdx.y * kAdRankTile, piece = lane & 7;
   if (r0 >= rank && r0 > 0) return;
-  const uint16_t* p[LOADS];
-  uint32_t on[LOADS];
+  const uint16_t* xp[2 * MT];
 #pragma unroll
-  for (int q = 0; q < LOADS; ++q) {
-    if (q < 2 * MT) {  // (a padding entry's product is not stored)
-      p[q] = a.x + (int64_t)(max(row_slot[q < 2 * MT ? q : 0], 0) / a.top_k) * a.ldx;
-      on[q] = ~0u;
-    } else {
-      const int j = r0 + (q - 2 * MT) * 8 + (lane >> 3);
-      p[q] = a.A + ((int64_t)w.adapter * a.r + (j < rank ? j : 0)) * a.K;
-      on[q] = j < rank ? ~0u : 0u;
-    }
+  for (int q = 0; q < 2 * MT; ++q)  // (a padding entry's product is not stored)
+    xp[q] = a.x + (int64_t)(max(row_slot[q], 0) / a.top_k) * a.ldx;
+  // (rows of A behind the adapter's own rank are read as they are: the second launch takes none of their sums)
+  const uint16_t* Aa = a.A + (int64_t)w.adapter * a.r * a.K;
+  uint32_t ar[2 * RT];
+#pragma unroll
+  for (int q = 0; q < 2 * RT; ++q) {
+    const int j = r0 + q * 8 + (lane >> 3);
+    ar[q] = (uint32_t)(j < a.r ? j : 0) * (uint32_t)a.K;
   }
   const int turns = (a.K + 255) >> 8;  // of the four waves
   const int lo = (int)((int64_t)turns * split / a.splits), hi = (int)((int64_t)turns * (split + 1) / a.splits);
@@ -119,9 +117,11 @@ __global__ __launch_bounds__(256) void adapters_inner_kernel(AdapterArgs a) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int k = (turn + u) * 256 + wv * 64 + piece * 8;
-      const bool in = turn + u < hi && k < a.K;  // (no branch around a load: what lies behind K is read elsewhere)
+      const uint32_t kk = k < a.K ? k : 0;  // (no branch around a load: what lies behind K is read elsewhere)
 #pragma unroll
-      for (int q = 0; q < LOADS; ++q) v[u][q] = mask4(*reinterpret_cast<const u32x4_t*>(p[q] + (in ? k : 0)), in ? on[q] : 0u);
+      for (int q = 0; q < 2 * MT; ++q) v[u][q] = *reinterpret_cast<const u32x4_t*>(xp[q] + kk);
+#pragma unroll
+      for (int q = 0; q < 2 * RT; ++q) v[u][2 * MT + q] = *reinterpret_cast<const u32x4_t*>(Aa + ar[q] + kk);
     }
   };
   f32x4_t acc[MT][RT];
@@ -134,9 +134,17 @@ __global__ __launch_bounds__(256) void adapters_inner_kernel(AdapterArgs a) {
   load(lo);
   for (int turn = lo; turn < hi; turn += UN) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u)
+    for (int u = 0; u < UN; ++u) {
+      // what lies behind K or the split is 0 in both operands (masked here: at the load it would be waited for there)
+      const int t = turn + u;
+      if (t >= hi || t * 256 + 256 > a.K) {
+        const uint32_t keep = t < hi && t * 256 + wv * 64 + piece * 8 < a.K ? ~0u : 0u;
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q) v[u][q] = v[u][q] & keep;
+      }
 #pragma unroll
       for (int q = 0; q < LOADS; ++q) *reinterpret_cast<u32x4_t*>(mine + (u * ROWS + q * 8) * 128) = v[u][q];
+    }
     if (turn + UN < hi) load(turn + UN);
     wave_lds_fence();
 #pragma unroll
@@ -201,9 +209,9 @@ __global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, i
   constexpr bool LINES = RT == 4;         // staged rows of eight pieces (8 ranks each), piece p of row i at p ^ (i & 7);
                                           // else of r / 8, as they lie in memory
   constexpr int PITCH = 68;               // values between staged rows of sums
-  constexpr int FRAG = MT * FR * 1024, BS = 64 * RT * 32, SUMS = 16 * PITCH * 4;
+  constexpr int FRAG = MT * FR * 1024, BS = 64 * RT * 32, SUMS = 16 * PITCH * 4, OWN = BS > SUMS ? BS : SUMS;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
-  __shared__ __attribute__((aligned(128))) uint8_t smem[FRAG + 4 * (BS + SUMS)];
+  __shared__ __attribute__((aligned(128))) uint8_t smem[FRAG + 4 * OWN];
   const int first = (int)a.row_blocks * strips;
   if ((int)blockIdx.x >= first) {
     copy_rows(a, (int64_t)(blockIdx.x - first) * 4 + wv, (int64_t)(gridDim.x - first) * 4);
@@ -211,8 +219,8 @@ __global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, i
   }
   const int tile_row = blockIdx.x / strips, strip = blockIdx.x - tile_row * strips;
   uint16_t* frag = reinterpret_cast<uint16_t*>(smem);  // [MT][parts][64][8]
-  uint8_t* bs = smem + FRAG + wv * (BS + SUMS);
-  float* sums = reinterpret_cast<float*>(bs + BS);
+  uint8_t* bs = smem + FRAG + wv * OWN;  // columns of B, then sums
+  float* sums = reinterpret_cast<float*>(bs);
   const RowTile w = row_tile(a, tile_row, 16 * MT);
   int slot[MT][2];  // of the rows that this lane loads and stores
 #pragma unroll
@@ -368,7 +376,8 @@ static int adapter_sizes(const char* fn, int64_t numel, int32_t L, int32_t r, in
               "%s: numel=%lld L=%d r=%d N=%d K=%d block_m=%d", fn, (long long)numel, L, r, N, K, block_m);
   MOE_REQUIRE(r % 8 == 0 && r <= kAdMaxRank && N % 8 == 0 && K % 8 == 0, MOE_EUNSUPPORTED,
               "%s: r=%d (at most %d), N=%d and K=%d must be multiples of 8", fn, r, kAdMaxRank, N, K);
-  MOE_REQUIRE((int64_t)N * r < (1ll << 30), MOE_EUNSUPPORTED, "%s: N=%d r=%d: an adapter of 2^30 values or more", fn, N, r);
+  MOE_REQUIRE((int64_t)std::max(N, K) * r < (1ll << 30), MOE_EUNSUPPORTED, "%s: N=%d K=%d r=%d: an adapter of 2^30 values or more",
+              fn, N, K, r);
   MOE_REQUIRE(L <= kAdMaxAdapters, MOE_EUNSUPPORTED, "%s: %d adapters (at most %d)", fn, L, kAdMaxAdapters);
   MOE_REQUIRE(numel < (1ll << 31) - 256 * kAdMaxAdapters, MOE_EUNSUPPORTED, "%s: numel=%lld too large", fn, (long long)numel);
   return MOE_OK;
