@@ -123,10 +123,15 @@ __device__ __forceinline__ float load_logit(const T* p) {
 template <int LANES>
 __device__ __forceinline__ int expert_of(int sub, int j) { return ((j / 4) * LANES + sub) * 4 + j % 4; }
 template <int LANES>
-__device__ __forceinline__ void place_of(int e, int& sub, int& j) {
-  sub = (e / 4) % LANES;
-  j = e / (4 * LANES) * 4 + e % 4;
+__device__ __forceinline__ void place_of(int expert, int& sub, int& j) {
+  const uint32_t e = (uint32_t)expert;
+  sub = (int)((e / 4) % LANES);
+  j = (int)(e / (4 * LANES) * 4 + e % 4);
 }
+// Experts j * LANES + sub, adjacent in a group, in LDS of [V][64]: the first's place for this lane, and the others' behind it.
+__device__ __forceinline__ int turned_place(uint32_t sub, uint32_t lane) { return (int)((sub & 3) * 64 + (lane - sub) + (sub >> 2)); }
+template <int LANES>
+__device__ __forceinline__ constexpr int turned_step(int j) { return (j / 4) * 256 + (j % 4) * (LANES / 4); }
 
 // A lane's logits (or biases, T float).  wide: rows aligned for loads of four, E a multiple of 4.  No branches around the loads: they would be waited for one by one,
 // so lanes without an expert read one that is there.
@@ -150,12 +155,9 @@ __device__ __forceinline__ void load_logits(const T* row, int sub, int E, bool w
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) x[j] = load_logit(row + min(j * LANES + sub, E - 1));
+    float* to = lds + turned_place(sub, lane);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      int s, i;
-      place_of<LANES>(j * LANES + sub, s, i);
-      lds[i * 64 + lane - sub + s] = x[j];
-    }
+    for (int j = 0; j < V; ++j) to[turned_step<LANES>(j)] = x[j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int j = 0; j < V; ++j) x[j] = lds[j * 64 + lane];
@@ -383,9 +385,9 @@ __device__ __forceinline__ int select_wide(const T* row, const float* bias, int 
 template <int IB, bool BIAS>
 struct Cut {
   static constexpr float kTop = (float)((1u << (32 - IB)) - 256), kStep = kTop / (BIAS ? 2.0f : 32.0f);
-  static __device__ __forceinline__ uint32_t key(float v, float off, int index) {
+  static __device__ __forceinline__ uint32_t key(float v, bool eligible, float off, int index) {
     const uint32_t q = (uint32_t)__builtin_amdgcn_fmed3f(fmaf(v, kStep, off), 1.0f, (float)((1u << (32 - IB)) - 1));
-    const uint32_t keep = v > -INFINITY ? ~0u : 0u;  // (a mask: a choice of the whole would become a branch)
+    const uint32_t keep = eligible & (v > -INFINITY) ? ~0u : 0u;  // (a mask: a choice of the whole would become a branch)
     return ((q << IB) | (uint32_t)index) & keep;
   }
 };
@@ -463,10 +465,7 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
             for (int j = 0; j < V; ++j) v[j] = biased(x[j], b[j], 0, m, inv);
           }
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            v[j] = x[j] > -INFINITY ? v[j] : -INFINITY;
-            top = fmaxf(top, v[j]);
-          }
+          for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);  // (of -inf logits too: it only places the range)
           top = group_max<LANES>(top);
           // A sigmoid is off by less than 5 * 2^-24 (its exponential by |x| 1.5 * 2^-24 and a unit, of which at most
           // 1.1 * 2^-24 remains, the sum and the reciprocal by a unit each), 2.5 steps of 2^-23; the sum
@@ -480,7 +479,7 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
         }
         off = Cut<IB, BIAS>::kTop - top * Cut<IB, BIAS>::kStep;  // (the same rounding for all of the row)
 #pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = Cut<IB, BIAS>::key(v[j], off, LAST - expert_of<LANES>(sub, j));
+        for (int j = 0; j < V; ++j) key[j] = Cut<IB, BIAS>::key(v[j], !BIAS || x[j] > -INFINITY, off, LAST - expert_of<LANES>(sub, j));
         // (the sorting leaves no registers: logits and biases are looked up again here)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -515,8 +514,8 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
           for (int j = 0; j < V; ++j) {
             const int c = expert_of<LANES>(sub, j);
             const float y = stash[j * 64], z = BIAS ? stash[(V + j) * 64] : 0.0f;
-            const float v = BIAS && y > -INFINITY ? biased(y, z, a.sigmoid, m, inv) : y;
-            if (Cut<IB, BIAS>::key(v, off, LAST - c) >= least) {
+            const float v = BIAS ? biased(y, z, a.sigmoid, m, inv) : y;
+            if (Cut<IB, BIAS>::key(v, !BIAS || y > -INFINITY, off, LAST - c) >= least) {
               const int at = atomicAdd(&lt.n[grp], 1);
               if (at < LANES) {
                 lt.expert[grp * LANES + at] = c;
@@ -790,12 +789,11 @@ __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradArgs a, int 
 #pragma unroll
   for (int j = 0; j < V; ++j) chosen[wv][j][lane] = out[j];
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const float* from = &chosen[wv][0][0] + turned_place(sub, lane);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int e = j * LANES + sub;
-    int s, i;
-    place_of<LANES>(e, s, i);
-    const float v = chosen[wv][i][lane - sub + s];
+    const float v = from[turned_step<LANES>(j)];
     if (e >= a.E) continue;
     if constexpr (std::is_same<T, float>::value) o[e] = v;
     else o[e] = f32_to_bf16(v);
