@@ -7,7 +7,12 @@
 // two bf16 halves, hi + lo, side by side along its K of 32 (16 ranks each), so the product of both costs no more
 // than a rank padded to 32 would.
 //
-// Bound: memory -- x is read once, base read and out written once, the adapters' rows once where rows are few.
+// Bound: memory -- x is read once, base read and out written once, the adapters' rows once where rows are few.  8179 rows,
+// most of them with one of 6 adapters of rank 64, K = N = 4096: 22 us (83 MB fetched, 4.0 TB/s) and 35 us (91 MB fetched, 67
+// written, 4.5 TB/s); 57 rows of as many adapters of rank 16, K 4096, N 8192: 5.4 and 7.5 us; one row 3.9 and 5.6 (launches, and
+// loads that wait for each other).
+//
+// An infinity in B meets the lower halves too, 0 or of either sign: its column may be NaN where the sum is infinite.
 #include <algorithm>
 #include <cmath>
 

@@ -3,9 +3,11 @@
 //   out = c sum_s g_s y_s:      dy_s = c g_s dout,  dg_s = c <dout, y_s>
 //   with a norm weight n:       z = y n,  r = (mean z^2 + eps)^-1/2,  out = c sum_s g_s r_s z_s,  d = <dout, z>
 //       dg_s = c r d,   dz = c g r (dout - (r^2 d / H) z),   dy = dz n,   dn = sum over the live slots of dz y
-// Dead slots: dy = 0, dg = 0, their y is not read.  fp32 throughout, each result rounded once.
+// Dead slots: dy = 0, dg = 0, what their y holds is not used.  fp32 throughout, each result rounded once.
 //
-// Bound: memory (every live row of y is read once, every row of dy written once).
+// Bound: memory (every live row of y is read once, every row of dy written once): 4096 tokens of 8 rows of 4096 columns
+// with the norm take 96 us, 5.1 TB/s of operands, and 4.6 for dn; with one pass in LDS and a second read (the general
+// kernel) 233 + 17.  2304 tokens of 2 rows of 512 take 4.3 us, mostly the launch.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -16,7 +18,8 @@ namespace moe {
 
 constexpr int kCgThreads = 256;
 constexpr int kCgMaxTopK = 16;
-constexpr int kCgParts = 512;      // workgroups that leave partial sums of dn, at most
+constexpr int kCgParts = 512;      // workgroups that leave partial sums of dn, at most (4096 x 8 x 4096: 256 take 112 us in the
+                                   // place of 96; 1024 no fewer, and dn 7.2 in the place of 4.6)
 constexpr int kCgGrid = 1 << 20;    // workgroups at most (2^32 threads are a launch's limit); they stay for more tokens
 constexpr int kCgMaxNormH = 12288; // columns whose dn a workgroup can hold in LDS
 
@@ -48,7 +51,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 }
 
 // A workgroup a token (or, with partial sums of dn, every gridDim.x-th one): the slots' sums first, then
-// the rows of dy, for which y and dout are read again.
+// the rows of dy, for which y and dout are read again.  The general form, for top_k > 8 and rows beyond 8192 columns.
 template <bool NORM>
 __global__ __launch_bounds__(kCgThreads) void combine_grad_kernel(CombineGradArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
