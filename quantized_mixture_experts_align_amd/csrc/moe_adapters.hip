@@ -2,19 +2,20 @@
 //     out[m] = base[m] + scale[a] * B_a (A_a x[m / top_k])      (a the adapter of row m)
 // over the align blocks of the rows' adapters.
 //
-// Two launches.  The first makes t = A_a x in fp32 (K split over waves, and over workgroups where there are
-// few rows), the second adds B_a t to the rows.  Between them t is not rounded to bf16: the matrix core gets it as
+// Two launches, or for few rows and short K one.  The first makes t = A_a x in fp32 (K split over waves, and over workgroups
+// where there are few rows), the second adds B_a t to the rows.  Between them t is not rounded to bf16: the matrix core gets it as
 // two bf16 halves, hi + lo, side by side along its K of 32 (16 ranks each), so the product of both costs no more
 // than a rank padded to 32 would.
 //
 // Bound: memory -- x is read once, base read and out written once, the adapters' rows once where rows are few.  8179 rows,
 // most of them with one of 6 adapters of rank 64, K = N = 4096: 22 us (83 MB fetched, 4.0 TB/s) and 35 us (91 MB fetched, 67
-// written, 4.5 TB/s); 57 rows of as many adapters of rank 16, K 4096, N 8192: 5.4 and 7.5 us; one row 3.9 and 5.6 (launches, and
-// loads that wait for each other).
+// written, 4.5 TB/s); 57 rows of as many adapters of rank 16, K 4096, N 8192: 5.4 and 7.5 us; one row of K 7168, N 4096
+// in one launch 8.2 (loads that wait for each other, and what one CU takes in).
 //
 // An infinity in B meets the lower halves too, 0 or of either sign: its column may be NaN where the sum is infinite.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_internal.h"
 
@@ -31,6 +32,7 @@ constexpr int kAdMaxAdapters = 512;
 // Workgroups that the two launches are split up to (8179 rows of rank 64 and 4096 columns: 256, 512, 768 of the first 32,
 // 24.5, 28 us; 512, 768, 1024, 1536 of the second 37, 40, 41, 45 us).
 constexpr int kAdGroups = 512, kAdStrips = 512;
+constexpr int kFewGroups = 256;  // of the one launch: one a CU, which its registers fill
 
 struct AdapterArgs {
   const uint16_t* x;
@@ -202,50 +204,35 @@ __device__ __forceinline__ void copy_rows(const AdapterArgs& a, int64_t first, i
   }
 }
 
-// out[m, n] = base[m, n] + sum_j B[a, n, j] scale[a] t[m, j].  The tile's t stands in LDS as the matrix core takes it:
-// for each 16 rows and 16 ranks, lane groups 0 and 1 the upper halves of ranks 0..7 and 8..15, groups 2 and 3 the
-// lower ones.  A wave makes 64 columns at a time.  Their columns of B (64 r values in a row, or 64 ranks of each at a time)
-// and the sums pass through places in LDS of the wave's own, so that all loads and stores are of whole lines by adjacent
-// lanes; the next columns' are in flight while these are made.  FR: 16-rank parts of t (r <= 16 FR).
+// Columns of out for a row tile: base + B t, t in LDS as the matrix core takes it: for each 16 rows and 16 ranks, lane groups 0
+// and 1 the upper halves of ranks 0..7 and 8..15, groups 2 and 3 the lower ones.  A wave makes 64 columns at a time.  Their
+// columns of B (64 r values in a row, or 64 ranks of each at a time) and the sums pass through places in LDS of the wave's
+// own, so that all loads and stores are of whole lines by adjacent lanes; the next columns' are in flight while these are made.
+// FR: 16-rank parts of t (r <= 16 FR).
 template <int MT, int FR>
-__global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, int strips) {
-  constexpr int RT = FR < 4 ? FR : 4;     // 16-rank parts that are staged at a time
-  constexpr int NL = 2 * RT;              // loads of them
-  constexpr bool LINES = RT == 4;         // staged rows of eight pieces (8 ranks each), piece p of row i at p ^ (i & 7);
-                                          // else of r / 8, as they lie in memory
-  constexpr int PITCH = 68;               // values between staged rows of sums
-  constexpr int FRAG = MT * FR * 1024, BS = 64 * RT * 32, SUMS = 16 * PITCH * 4, OWN = BS > SUMS ? BS : SUMS;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
-  __shared__ __attribute__((aligned(128))) uint8_t smem[FRAG + 4 * OWN];
-  const int first = (int)a.row_blocks * strips;
-  if ((int)blockIdx.x >= first) {
-    copy_rows(a, (int64_t)(blockIdx.x - first) * 4 + wv, (int64_t)(gridDim.x - first) * 4);
-    return;
-  }
-  const int tile_row = blockIdx.x / strips, strip = blockIdx.x - tile_row * strips;
-  uint16_t* frag = reinterpret_cast<uint16_t*>(smem);  // [MT][parts][64][8]
-  uint8_t* bs = smem + FRAG + wv * OWN;  // columns of B, then sums
-  float* sums = reinterpret_cast<float*>(bs);
-  const RowTile w = row_tile(a, tile_row, 16 * MT);
+struct Columns {
+  static constexpr int RT = FR < 4 ? FR : 4;     // 16-rank parts that are staged at a time
+  static constexpr int NL = 2 * RT;              // loads of them
+  static constexpr bool LINES = RT == 4;         // staged rows of eight pieces (8 ranks each), piece p of row i at p ^ (i & 7);
+                                                 // else of r / 8, as they lie in memory
+  static constexpr int PITCH = 68;               // values between staged rows of sums
+  static constexpr int FRAG = MT * FR * 1024, BS = 64 * RT * 32, SUMS = 16 * PITCH * 4, OWN = BS > SUMS ? BS : SUMS;
+  const AdapterArgs& a;
+  const uint16_t* Ba;    // the adapter's B
+  const uint16_t* frag;  // [MT][parts][64][8]
+  uint8_t* bs;           // the wave's own OWN bytes
+  int lane, rank;
   int slot[MT][2];  // of the rows that this lane loads and stores
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) slot[m][h] = slot_of(a, w, m * 16 + h * 8 + (lane >> 3));
-  if (w.adapter < 0) return;
-  const int rank = adapter_rank(a, w.adapter), RK = (rank + 15) >> 4;
-  const float scale = a.scales ? a.scales[w.adapter] : 1.0f;
-  const uint16_t* Ba = a.B + (int64_t)w.adapter * a.N * a.r;
-  // the first columns of base and B
-  const int col = (lane & 7) * 8, pieces = a.r / 8;
   u32x4_t base[MT][2], bv[NL];
+
   // (No branches around loads, and none of them left out: columns behind N are read again and not stored.  The waits count
   // what is in flight, and would else count on none of it.)
-  const uint32_t last_col = (uint32_t)a.N - 8, last_b = (uint32_t)a.N * (uint32_t)a.r - 8;
-  auto load_base = [&](int n0, int m, int h) __attribute__((always_inline)) {
-    base[m][h] = *reinterpret_cast<const u32x4_t*>(a.base + (int64_t)max(slot[m][h], 0) * a.ldb + min((uint32_t)(n0 + col), last_col));
-  };
-  auto load_b = [&](int n0, int c0) __attribute__((always_inline)) {
+  __device__ __forceinline__ void load_base(int n0, int m, int h) {
+    base[m][h] = *reinterpret_cast<const u32x4_t*>(a.base + (int64_t)max(slot[m][h], 0) * a.ldb +
+                                                   min((uint32_t)(n0 + (lane & 7) * 8), (uint32_t)a.N - 8));
+  }
+  __device__ __forceinline__ void load_b(int n0, int c0) {
+    const uint32_t last_b = (uint32_t)a.N * (uint32_t)a.r - 8;
 #pragma unroll
     for (int q = 0; q < NL; ++q) {
       const uint32_t i = q * 64 + lane;  // piece of the staged ones
@@ -258,13 +245,113 @@ __global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, i
       }
       bv[q] = *reinterpret_cast<const u32x4_t*>(Ba + at);
     }
-  };
-  int n0 = (strip * 4 + wv) * 64;
-  load_b(n0, 0);
+  }
+  __device__ __forceinline__ void load(int n0) {
+    load_b(n0, 0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_base(n0, m, h);
+  }
+  // The columns n0, n0 + step, ..., of which the first have been asked for.
+  __device__ __forceinline__ void add(int n0, int step) {
+    const int l16 = lane & 15, g = lane >> 4, col = (lane & 7) * 8, pieces = a.r / 8, RK = (rank + 15) >> 4;
+    float* sums = reinterpret_cast<float*>(bs);
+    for (; n0 < a.N; n0 += step) {
+      f32x4_t acc[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[m][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int c0 = 0; c0 < (FR <= 4 ? 1 : RK); c0 += RT) {
+        if (c0) load_b(n0, c0);
+#pragma unroll
+        for (int q = 0; q < NL; ++q)
+          if (LINES || q * 64 + lane < 64 * pieces) *reinterpret_cast<u32x4_t*>(bs + (q * 64 + lane) * 16) = bv[q];
+        if (FR <= 4 || c0 + RT >= RK) load_b(n0 + step, 0);
+        wave_lds_fence();
+#pragma unroll
+        for (int c = 0; c < RT; ++c) {
+          if (c0 + c >= RK) continue;
+          const int pc = 2 * c + (g & 1), left = rank - (c0 + c) * 16 - (g & 1) * 8;
+          uint32_t keep[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) keep[j] = 2 * j + 1 < left ? ~0u : (2 * j < left ? 0xFFFFu : 0u);
+          bf16x8_t bf[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = u * 16 + l16, at = LINES ? row * 8 + (pc ^ (row & 7)) : row * pieces + min(pc, pieces - 1);
+            const u32x4_t r = *reinterpret_cast<const u32x4_t*>(bs + at * 16);  // (values behind the adapter's own rank as 0)
+            bf[u] = __builtin_bit_cast(bf16x8_t, u32x4_t{r[0] & keep[0], r[1] & keep[1], r[2] & keep[2], r[3] & keep[3]});
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const bf16x8_t tv = *reinterpret_cast<const bf16x8_t*>(frag + ((int64_t)(m * RK + c0 + c) * 64 + lane) * 8);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[u], tv, acc[m][u], 0, 0, 0);
+          }
+        }
+        wave_lds_fence();
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) *reinterpret_cast<f32x4_t*>(sums + l16 * PITCH + u * 16 + g * 4) = acc[m][u];
+        wave_lds_fence();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float* o = sums + (h * 8 + (lane >> 3)) * PITCH + col;
+          const f32x4_t p = *reinterpret_cast<const f32x4_t*>(o), q = *reinterpret_cast<const f32x4_t*>(o + 4);
+          const u32x4_t b = base[m][h];
+          // (past the L2, which keeps the operands: 62 -> 56 us for both launches on 8179 rows of 4096 columns)
+          if (slot[m][h] >= 0 && n0 + col < a.N)
+            __builtin_nontemporal_store(
+                u32x4_t{pack_bf16x2(bf16_lo(b[0]) + p[0], bf16_hi(b[0]) + p[1]), pack_bf16x2(bf16_lo(b[1]) + p[2], bf16_hi(b[1]) + p[3]),
+                        pack_bf16x2(bf16_lo(b[2]) + q[0], bf16_hi(b[2]) + q[1]), pack_bf16x2(bf16_lo(b[3]) + q[2], bf16_hi(b[3]) + q[3])},
+                reinterpret_cast<u32x4_t*>(a.out + (int64_t)slot[m][h] * a.ldo + n0 + col));
+          load_base(n0 + step, m, h);
+        }
+        wave_lds_fence();
+      }
+    }
+  }
+};
+// Two values of t, scaled, and their lower halves.
+__device__ __forceinline__ void halves(float p, float q, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(p, q);
+  const float dp = p - bf16_lo(hi), dq = q - bf16_hi(hi);  // (an infinity has no lower half)
+  lo = pack_bf16x2(fabsf(dp) < INFINITY ? dp : 0.0f, fabsf(dq) < INFINITY ? dq : 0.0f);
+}
+
+// out[m, n] = base[m, n] + sum_j B[a, n, j] scale[a] t[m, j].
+template <int MT, int FR>
+__global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, int strips) {
+  using Cols = Columns<MT, FR>;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  __shared__ __attribute__((aligned(128))) uint8_t smem[Cols::FRAG + 4 * Cols::OWN];
+  const int first = (int)a.row_blocks * strips;
+  if ((int)blockIdx.x >= first) {
+    copy_rows(a, (int64_t)(blockIdx.x - first) * 4 + wv, (int64_t)(gridDim.x - first) * 4);
+    return;
+  }
+  const int tile_row = blockIdx.x / strips, strip = blockIdx.x - tile_row * strips;
+  uint16_t* frag = reinterpret_cast<uint16_t*>(smem);
+  const RowTile w = row_tile(a, tile_row, 16 * MT);
+  int slot[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) load_base(n0, m, h);
+    for (int h = 0; h < 2; ++h) slot[m][h] = slot_of(a, w, m * 16 + h * 8 + (lane >> 3));
+  if (w.adapter < 0) return;
+  const int rank = adapter_rank(a, w.adapter), RK = (rank + 15) >> 4;
+  const float scale = a.scales ? a.scales[w.adapter] : 1.0f;
+  Cols cols{a, a.B + (int64_t)w.adapter * a.N * a.r, frag, smem + Cols::FRAG + wv * Cols::OWN, lane, rank};
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) cols.slot[m][h] = slot[m][h];
+  const int n0 = (strip * 4 + wv) * 64;
+  cols.load(n0);
   // t: eight ranks of a row for each P adjacent threads, which share the splits
   const int items = MT * RK * 32;
   int P = 1;
@@ -291,75 +378,121 @@ __global__ __launch_bounds__(256, 2) void adapters_outer_kernel(AdapterArgs a, i
       for (int j = 0; j < 8; ++j) v[j] += __shfl_xor(v[j], d);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float p = j0 + 2 * j < rank ? v[2 * j] * scale : 0.0f, q = j0 + 2 * j + 1 < rank ? v[2 * j + 1] * scale : 0.0f;
-      hi[j] = pack_bf16x2(p, q);
-      const float dp = p - bf16_lo(hi[j]), dq = q - bf16_hi(hi[j]);  // (an infinity has no lower half)
-      lo[j] = pack_bf16x2(fabsf(dp) < INFINITY ? dp : 0.0f, fabsf(dq) < INFINITY ? dq : 0.0f);
-    }
+    for (int j = 0; j < 4; ++j)
+      halves(j0 + 2 * j < rank ? v[2 * j] * scale : 0.0f, j0 + 2 * j + 1 < rank ? v[2 * j + 1] * scale : 0.0f, hi[j], lo[j]);
     uint16_t* d = frag + (int64_t)tile * 512 + (half * 16 + l) * 8;
     if (part == 0) *reinterpret_cast<u32x4_t*>(d) = u32x4_t{hi[0], hi[1], hi[2], hi[3]};
     if (part == P - 1) *reinterpret_cast<u32x4_t*>(d + 256) = u32x4_t{lo[0], lo[1], lo[2], lo[3]};
   }
   __syncthreads();
-  const int step = strips * 256;
-  for (; n0 < a.N; n0 += step) {
-    f32x4_t acc[MT][4];
+  cols.add(n0, strips * 256);
+}
+
+// Both products in one launch, for tiles of 16 rows and r <= 16 RT: every workgroup of a tile makes all of t for itself.  Its
+// eight waves take 64 k of every row in turn, UN turns' loads in flight a wave, through the wave's own LDS as above.
+constexpr int kFewWaves = 8;
+template <int RT, int UN>
+__global__ __launch_bounds__(kFewWaves * 64) void adapters_few_kernel(AdapterArgs a, int strips) {
+  using Cols = Columns<1, RT>;
+  constexpr int W = kFewWaves, ROWS = 16 * (1 + RT), LOADS = ROWS / 8;
+  constexpr int STAGE = ROWS * 128, PLACE = STAGE > Cols::OWN ? STAGE : Cols::OWN;  // a wave's (the sums need RT * 1024)
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, g = lane >> 4, piece = lane & 7;
+  __shared__ __attribute__((aligned(128))) uint8_t smem[Cols::FRAG + W * PLACE];
+  const int first = (int)a.row_blocks * strips;
+  if ((int)blockIdx.x >= first) {
+    copy_rows(a, (int64_t)(blockIdx.x - first) * W + wv, (int64_t)(gridDim.x - first) * W);
+    return;
+  }
+  const int tile = blockIdx.x / strips, strip = blockIdx.x - tile * strips;
+  const RowTile w = row_tile(a, tile, 16);
+  const int slot[2] = {slot_of(a, w, lane >> 3), slot_of(a, w, 8 + (lane >> 3))};
+  if (w.adapter < 0) return;
+  const int rank = adapter_rank(a, w.adapter);
+  const float scale = a.scales ? a.scales[w.adapter] : 1.0f;
+  uint16_t* frag = reinterpret_cast<uint16_t*>(smem);
+  uint8_t* place = smem + Cols::FRAG + wv * PLACE;
+  Cols cols{a, a.B + (int64_t)w.adapter * a.N * a.r, frag, place, lane, rank, {{slot[0], slot[1]}}};
+  const int n0 = (strip * W + wv) * 64;
+  cols.load(n0);
+  const uint16_t* from[LOADS];  // (a padding entry's product is not stored, nor what stands behind the adapter's own rank used)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int q = 0; q < 2; ++q) from[q] = a.x + (int64_t)(max(slot[q], 0) / a.top_k) * a.ldx;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) acc[m][u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 0; c0 < (FR <= 4 ? 1 : RK); c0 += RT) {
-      if (c0) load_b(n0, c0);
+  for (int q = 0; q < 2 * RT; ++q) {
+    const int j = q * 8 + (lane >> 3);
+    from[2 + q] = a.A + (int64_t)w.adapter * a.r * a.K + (uint32_t)(j < a.r ? j : 0) * (uint32_t)a.K;
+  }
+  f32x4_t acc[RT];
 #pragma unroll
-      for (int q = 0; q < NL; ++q)
-        if (LINES || q * 64 + lane < 64 * pieces) *reinterpret_cast<u32x4_t*>(bs + (q * 64 + lane) * 16) = bv[q];
-      if (FR <= 4 || c0 + RT >= RK) load_b(n0 + step, 0);
-      wave_lds_fence();
+  for (int j = 0; j < RT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint8_t* mine = place + (lane >> 3) * 128 + (piece ^ (lane >> 3)) * 16;
+  const int turns = (a.K + 63) >> 6;
+  // (X: loads of rows of x.  A tile of 8 rows or fewer leaves the second out: half of what a single row's tile would load were copies of it.)
+  auto product = [&](auto x_loads) __attribute__((always_inline)) {
+    constexpr int X = decltype(x_loads)::value;
+    u32x4_t v[UN][LOADS];
+    auto load = [&](int turn, int u) __attribute__((always_inline)) {
+      const int k = turn * 64 + piece * 8;
+      const uint32_t kk = k < a.K ? k : 0;  // (what lies behind K is read elsewhere; its product is masked)
 #pragma unroll
-      for (int c = 0; c < RT; ++c) {
-        if (c0 + c >= RK) continue;
-        const int pc = 2 * c + (g & 1), left = rank - (c0 + c) * 16 - (g & 1) * 8;
-        uint32_t keep[4];
+      for (int q = 0; q < LOADS; ++q)
+        if (q < X || q >= 2) v[u][q] = *reinterpret_cast<const u32x4_t*>(from[q] + kk);
+    };
+    auto multiply = [&](int turn, int u) __attribute__((always_inline)) {
+      const uint32_t keep = turn * 64 + piece * 8 < a.K ? ~0u : 0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) keep[j] = 2 * j + 1 < left ? ~0u : (2 * j < left ? 0xFFFFu : 0u);
-        bf16x8_t bf[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int row = u * 16 + l16, at = LINES ? row * 8 + (pc ^ (row & 7)) : row * pieces + min(pc, pieces - 1);
-          const u32x4_t r = *reinterpret_cast<const u32x4_t*>(bs + at * 16);  // (values behind the adapter's own rank as 0)
-          bf[u] = __builtin_bit_cast(bf16x8_t, u32x4_t{r[0] & keep[0], r[1] & keep[1], r[2] & keep[2], r[3] & keep[3]});
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const bf16x8_t tv = *reinterpret_cast<const bf16x8_t*>(frag + ((int64_t)(m * RK + c0 + c) * 64 + lane) * 8);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) acc[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[u], tv, acc[m][u], 0, 0, 0);
-        }
-      }
-      wave_lds_fence();
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) *reinterpret_cast<f32x4_t*>(sums + l16 * PITCH + u * 16 + g * 4) = acc[m][u];
+      for (int q = 0; q < LOADS; ++q)
+        if (q < X || q >= 2) *reinterpret_cast<u32x4_t*>(mine + q * 1024) = v[u][q] & keep;
       wave_lds_fence();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float* o = sums + (h * 8 + (lane >> 3)) * PITCH + col;
-        const f32x4_t p = *reinterpret_cast<const f32x4_t*>(o), q = *reinterpret_cast<const f32x4_t*>(o + 4);
-        const u32x4_t b = base[m][h];
-        // (past the L2, which keeps the operands: 62 -> 56 us for both launches on 8179 rows of 4096 columns)
-        if (slot[m][h] >= 0 && n0 + col < a.N)
-          __builtin_nontemporal_store(
-              u32x4_t{pack_bf16x2(bf16_lo(b[0]) + p[0], bf16_hi(b[0]) + p[1]), pack_bf16x2(bf16_lo(b[1]) + p[2], bf16_hi(b[1]) + p[3]),
-                         pack_bf16x2(bf16_lo(b[2]) + q[0], bf16_hi(b[2]) + q[1]), pack_bf16x2(bf16_lo(b[3]) + q[2], bf16_hi(b[3]) + q[3])},
-              reinterpret_cast<u32x4_t*>(a.out + (int64_t)slot[m][h] * a.ldo + n0 + col));
-        load_base(n0 + step, m, h);
+        const uint8_t* at = place + l16 * 128 + ((4 * h + g) ^ (l16 & 7)) * 16;
+        const bf16x8_t xf = *reinterpret_cast<const bf16x8_t*>(at);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          const bf16x8_t af = *reinterpret_cast<const bf16x8_t*>(at + (1 + j) * 2048);
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af, xf, acc[j], 0, 0, 0);
+        }
       }
       wave_lds_fence();
+    };
+    int turn = wv;
+    for (; turn + (UN - 1) * W < turns; turn += UN * W) {
+#pragma unroll
+      for (int u = 0; u < UN; ++u) load(turn + u * W, u);
+#pragma unroll
+      for (int u = 0; u < UN; ++u) multiply(turn + u * W, u);
     }
+#pragma unroll
+    for (int u = 0; u < UN - 1; ++u)
+      if (turn + u * W < turns) load(turn + u * W, u);
+#pragma unroll
+    for (int u = 0; u < UN - 1; ++u)
+      if (turn + u * W < turns) multiply(turn + u * W, u);
+  };
+  if (__any(slot[1] >= 0)) product(std::integral_constant<int, 2>{});
+  else product(std::integral_constant<int, 1>{});
+  __syncthreads();
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(smem + Cols::FRAG);
+#pragma unroll
+  for (int j = 0; j < RT; ++j) red[(wv * RT + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  // ranks 4 g .. 4 g + 3 of a part for a row, each to its place among the halves
+  if (wv < RT) {
+    f32x4_t t = red[wv * 64 + lane];
+#pragma unroll
+    for (int i = 1; i < W; ++i) t += red[(i * RT + wv) * 64 + lane];
+    const int c = wv * 16 + g * 4;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      halves(c + 2 * j < rank ? t[2 * j] * scale : 0.0f, c + 2 * j + 1 < rank ? t[2 * j + 1] * scale : 0.0f, hi[j], lo[j]);
+    uint16_t* d = frag + wv * 512 + ((g >> 1) * 16 + l16) * 8 + (g & 1) * 4;
+    *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(d + 256) = make_uint2(lo[0], lo[1]);
   }
+  __syncthreads();
+  cols.add(n0, strips * W * 64);
 }
 
 // Rows of a workgroup's tile, row tiles of the batch (at most), and splits of K: about 512 workgroups, each with a turn
@@ -398,8 +531,29 @@ static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st
   hipLaunchKernelGGL((adapters_outer_kernel<MT, FR>), dim3((unsigned)(a.row_blocks * strips + copies)), dim3(256), 0, st, a,
                      (int)strips);
 }
+// Where one launch is the better: the workgroups of a row tile each make all of its t, at some 110 GB/s, so few tiles and short
+// rows of A.  Against two launches, replayed from a graph, rank 16, N 4096, one row: K 512 4.3 us against 6.7, 2048 5.4 and 7.2, 4096 6.6 and
+// 7.6, 7168 8.2 and 8.1, 14336 12.3 and 7.2; rank 32: 2048 6.8 and 8.1, 4096 8.6 and 8.0.  16 rows of 8 adapters: the same up to 4096, 7168
+// 9.8 and 8.4; 32 of 32: 2048 9.9 and 7.9; 64 of 64, K 512: 5.1 and 7.5; 256 of 256, K 512: 9.0 and 11.4.  (Calls that are not captured
+// save the second launch's 3 us of host time besides.)
+static bool few_rows(const AdapterArgs& a) {
+  const int64_t padded = a.r <= 16 ? 16 : 32;
+  return a.r <= 32 && (a.row_blocks <= 16 ? padded * a.K < (1 << 17) : a.K <= 512);
+}
+template <int RT, int UN>
+static void launch_few(const AdapterArgs& a, int64_t copies, hipStream_t st) {
+  constexpr int COLS = kFewWaves * 64;
+  const int64_t strips = std::max<int64_t>(1, std::min<int64_t>((a.N + COLS - 1) / COLS, (kFewGroups + a.row_blocks - 1) / a.row_blocks));
+  hipLaunchKernelGGL((adapters_few_kernel<RT, UN>), dim3((unsigned)(a.row_blocks * strips + copies)), dim3(kFewWaves * 64), 0, st, a,
+                     (int)strips);
+}
 template <int MT>
 static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st) {
+  if (MT == 1 && few_rows(a)) {
+    if (a.r <= 16) launch_few<1, 8>(a, copies, st);
+    else launch_few<2, 6>(a, copies, st);
+    return;
+  }
   constexpr int UN = MT == 1 ? 2 : 1;
   if (a.r <= 16) launch_adapters<MT, 1, 1, UN>(a, copies, st);
   else if (a.r <= 32) launch_adapters<MT, 2, 2, UN>(a, copies, st);

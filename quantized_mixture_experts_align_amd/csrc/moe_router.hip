@@ -389,7 +389,7 @@ struct Cut {
   static constexpr float kTop = (float)((1u << (32 - IB)) - 256), kStep = kTop / (BIAS ? 2.0f : 32.0f);
   static __device__ __forceinline__ uint32_t key(float v, bool eligible, float off, int index) {
     const uint32_t q = (uint32_t)__builtin_amdgcn_fmed3f(fmaf(v, kStep, off), 1.0f, (float)((1u << (32 - IB)) - 1));
-    const uint32_t keep = eligible & (v > -INFINITY) ? ~0u : 0u;  // (a mask: a choice of the whole would become a branch)
+    const uint32_t keep = (eligible & (v > -INFINITY)) ? ~0u : 0u;  // (a mask: a choice of the whole would become a branch)
     return ((q << IB) | (uint32_t)index) & keep;
   }
 };
