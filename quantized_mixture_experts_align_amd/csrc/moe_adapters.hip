@@ -537,8 +537,8 @@ static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st
 // 9.8 and 8.4; 32 of 32: 2048 9.9 and 7.9; 64 of 64, K 512: 5.1 and 7.5; 256 of 256, K 512: 9.0 and 11.4.  (Calls that are not captured
 // save the second launch's 3 us of host time besides.)
 static bool few_rows(const AdapterArgs& a) {
-  const int64_t padded = a.r <= 16 ? 16 : 32;
-  return a.r <= 32 && (a.row_blocks <= 16 ? padded * a.K < (1 << 17) : a.K <= 512);
+  const int64_t values = (int64_t)(a.r <= 16 ? 16 : 32) * a.K;
+  return a.r <= 32 && (a.row_blocks == 1 ? values < (1 << 17) : a.row_blocks <= 16 ? values <= (1 << 16) : a.K <= 512);
 }
 template <int RT, int UN>
 static void launch_few(const AdapterArgs& a, int64_t copies, hipStream_t st) {

@@ -42,7 +42,8 @@ SIZES = [(1, 1, 8, 8, 8, 16), (1, 8, 16, 4096, 7168, 16), (3, 4, 24, 72, 40, 1),
          (40, 5, 40, 520, 136, 17), (100, 4, 64, 256, 512, 32), (300, 3, 64, 1000, 264, 64), (257, 2, 72, 88, 328, 100),
          (500, 6, 128, 136, 96, 256), (90, 3, 200, 328, 200, 16), (140, 2, 256, 264, 520, 64), (2000, 7, 16, 136, 72, 64),
          (700, 512, 8, 64, 64, 16), (20, 1, 16, 24, 24, 48), (9, 3, 32, 520, 2056, 16), (30, 12, 16, 1032, 4104, 8),
-         (16, 1, 16, 8200, 8184, 16), (300, 40, 24, 600, 504, 16), (600, 40, 32, 88, 520, 16)]
+         (16, 1, 16, 8200, 8184, 16), (300, 40, 24, 600, 504, 16), (600, 40, 32, 88, 520, 16),
+         (9, 3, 32, 520, 2040, 16), (5, 1, 32, 264, 4088, 16), (30, 12, 16, 1032, 4096, 8)]
 
 
 @pytest.mark.parametrize("numel,n,r,N,K,B", SIZES)
