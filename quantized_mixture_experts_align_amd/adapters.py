@@ -36,8 +36,8 @@ def moe_adapters_add(base: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: to
     float32 [n] (1 without), ranks int32 [n] (adapters of fewer than r ranks: what stands behind is not used).
 
     `align` is what moe_align returns for the rows' adapter ids [numel, 1] (expert_start 0, n_local n) with the same
-    block_m.  `out`: base itself, or memory apart from it (allocated when not given).  `work`: float32 workspace of
-    adapters_workspace(numel, n, r, K, block_m) values (allocated when not given)."""
+    block_m.  `out`: base itself, or memory apart from it (allocated when not given); it may be x or lie over it.
+    `work`: float32 workspace of adapters_workspace(numel, n, r, K, block_m) values (allocated when not given)."""
     _check(base, "base", _BF16, rows=True)
     dev, (numel, N) = base.device, base.shape
     _check(x, "x", _BF16, dev=dev, rows=True)

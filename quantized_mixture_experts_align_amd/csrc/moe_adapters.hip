@@ -50,6 +50,7 @@ struct AdapterArgs {
   int32_t top_k, block_m, per, splits;  // per: row tiles of an align block
   int64_t row_blocks;
   float* t;  // [splits][numel][r]
+  bool over_x;  // out may hold rows of x
 };
 
 __device__ __forceinline__ int adapter_rank(const AdapterArgs& a, int ad) {
@@ -509,6 +510,14 @@ static int adapter_splits(int64_t row_blocks, int r, int K) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({kAdGroups / groups, by_k, kAdMaxSplits}));
 }
 
+// Whether the rows from p on reach into the memory between the first and the last of those from q on.
+static bool rows_meet(const uint16_t* p, int64_t rows, int64_t ld, int32_t cols, const uint16_t* q, int64_t rows_q, int64_t ld_q,
+                      int32_t cols_q) {
+  const uintptr_t p0 = (uintptr_t)p, p1 = p0 + ((rows - 1) * ld + cols) * 2, q0 = (uintptr_t)q,
+                  q1 = q0 + ((rows_q - 1) * ld_q + cols_q) * 2;
+  return p0 < q1 && q0 < p1;
+}
+
 static int adapter_sizes(const char* fn, int64_t numel, int32_t L, int32_t r, int32_t N, int32_t K, int32_t block_m) {
   MOE_REQUIRE(numel >= 0 && L >= 1 && r >= 1 && N >= 1 && K >= 1 && block_m >= 1 && block_m <= 256, MOE_EINVAL,
               "%s: numel=%lld L=%d r=%d N=%d K=%d block_m=%d", fn, (long long)numel, L, r, N, K, block_m);
@@ -531,14 +540,15 @@ static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st
   hipLaunchKernelGGL((adapters_outer_kernel<MT, FR>), dim3((unsigned)(a.row_blocks * strips + copies)), dim3(256), 0, st, a,
                      (int)strips);
 }
-// Where one launch is the better: the workgroups of a row tile each make all of its t, at some 110 GB/s, so few tiles and short
+// Where one launch is the better, and right: a workgroup that has stored its columns must not have stored over x, which the tile's
+// other workgroups may still be reading (two launches are done with x before the first store).  The workgroups of a row tile each make all of its t, at some 110 GB/s, so few tiles and short
 // rows of A.  Against two launches, replayed from a graph, rank 16, N 4096, one row: K 512 4.3 us against 6.7, 2048 5.4 and 7.2, 4096 6.6 and
 // 7.6, 7168 8.2 and 8.1, 14336 12.3 and 7.2; rank 32: 2048 6.8 and 8.1, 4096 8.6 and 8.0.  16 rows of 8 adapters: the same up to 4096, 7168
 // 9.8 and 8.4; 32 of 32: 2048 9.9 and 7.9; 64 of 64, K 512: 5.1 and 7.5; 256 of 256, K 512: 9.0 and 11.4.  (Calls that are not captured
 // save the second launch's 3 us of host time besides.)
 static bool few_rows(const AdapterArgs& a) {
   const int64_t values = (int64_t)(a.r <= 16 ? 16 : 32) * a.K;
-  return a.r <= 32 && (a.row_blocks == 1 ? values < (1 << 17) : a.row_blocks <= 16 ? values <= (1 << 16) : a.K <= 512);
+  return !a.over_x && a.r <= 32 && (a.row_blocks == 1 ? values < (1 << 17) : a.row_blocks <= 16 ? values <= (1 << 16) : a.K <= 512);
 }
 template <int RT, int UN>
 static void launch_few(const AdapterArgs& a, int64_t copies, hipStream_t st) {
@@ -598,16 +608,15 @@ extern "C" int moe_adapters_add(const uint16_t* base, int64_t ld_base, const uin
   if (in_place) {
     MOE_REQUIRE(ld_out == ld_base, MOE_EINVAL, "moe_adapters_add: out is base with another leading dimension");
   } else {
-    const uintptr_t b0 = (uintptr_t)base, b1 = b0 + ((numel - 1) * ld_base + N) * 2, o0 = (uintptr_t)out,
-                    o1 = o0 + ((numel - 1) * ld_out + N) * 2;
-    MOE_REQUIRE(o1 <= b0 || b1 <= o0, MOE_EINVAL, "moe_adapters_add: out overlaps base");
+    MOE_REQUIRE(!rows_meet(out, numel, ld_out, N, base, numel, ld_base, N), MOE_EINVAL, "moe_adapters_add: out overlaps base");
   }
   MOE_REQUIRE((((uintptr_t)base | (uintptr_t)x | (uintptr_t)A | (uintptr_t)B | (uintptr_t)out | (uintptr_t)work) & 15) == 0 &&
                   (((uintptr_t)scales | (uintptr_t)ranks | (uintptr_t)sorted_token_ids | (uintptr_t)adapter_ids |
                     (uintptr_t)num_tokens_post_padded | (uintptr_t)slot_local_ids) & 3) == 0,
               MOE_EUNSUPPORTED, "moe_adapters_add: bf16 tensors and the workspace must be 16-byte aligned, the others 4");
   AdapterArgs a{x, ld_x, A, B, scales, ranks, L, r, N, K, base, ld_base, out, ld_out, sorted_token_ids, adapter_ids,
-                num_tokens_post_padded, slot_local_ids, numel, top_k, block_m, 1, 1, 0, work};
+                num_tokens_post_padded, slot_local_ids, numel, top_k, block_m, 1, 1, 0, work,
+                rows_meet(out, numel, ld_out, N, x, (numel + top_k - 1) / top_k, ld_x, K)};
   a.row_blocks = adapter_row_blocks(numel, L, block_m, &a.per);
   a.splits = adapter_splits(a.row_blocks, r, K);
   MOE_REQUIRE(work_elems >= a.splits * numel * r, MOE_ESIZE, "moe_adapters_add: workspace of %lld values, need %lld",

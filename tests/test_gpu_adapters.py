@@ -96,6 +96,30 @@ def test_strided_rows_and_padding_columns():
     assert torch.equal(inner, got)
 
 
+@pytest.mark.parametrize("numel,n,r,N,B", [(1, 1, 16, 4096, 16), (16, 8, 16, 1032, 16), (40, 3, 32, 512, 16), (70, 5, 24, 1544, 16),
+                                           (9, 3, 32, 4096, 16), (64, 64, 16, 8192, 16), (100, 4, 64, 776, 64)])
+def test_out_over_x(numel, n, r, N, B):
+    """x += B A x in place, and out over x with base elsewhere: all of x is read before a column is written."""
+    d = make(numel, n, r, N, N, 3 * numel + r)
+    announce(f"over x: numel={numel} n={n} r={r} N=K={N} B={B}")
+    h = d["x"].cuda()
+    assert call(d, B, base=h, x=h, out=h) is h
+    check({**d, "base": d["x"]}, h, "base = x = out")
+    h = d["x"].cuda()
+    call(d, B, x=h, out=h)
+    check(d, h, "x = out")
+    both = torch.empty((numel + 3, N), dtype=torch.bfloat16, device="cuda")
+    x = both[3:].copy_(d["x"])
+    check(d, call(d, B, x=x, out=both[:-3]), "out ends in x")
+
+
+def test_out_over_x_of_several_choices():
+    d = make(48, 5, 16, 1032, 1032, 23, top_k=2)
+    out = torch.empty((48, 1032), dtype=torch.bfloat16, device="cuda")
+    x = out[20:44].copy_(d["x"])
+    check(d, call(d, 16, x=x, out=out), "out around x")
+
+
 def test_no_row_all_rows_and_one_row_of_an_adapter():
     for none in (1.0, 0.0):
         d = make(33, 3, 8, 64, 64, 12, none=none)
