@@ -323,8 +323,8 @@ __device__ __forceinline__ double exp_wide(double x) {
   return ldexp(p / 87178291200.0, (int)n);
 }
 
-// The 64-bit key of an expert (0: not eligible): its logit with the index behind it, or its biased score in 64 bits
-// whose lowest 10 places give way to the index.
+// The 64-bit key of an expert (0: not eligible): its logit with the index behind it, or its biased score, whole (equal
+// scores go by the index all the same).
 template <bool BIAS>
 __device__ __forceinline__ uint64_t wide_key(float x, float b, int e, int sigmoid, float m, double total) {
   if (!(x > -INFINITY)) return 0;
@@ -332,7 +332,7 @@ __device__ __forceinline__ uint64_t wide_key(float x, float b, int e, int sigmoi
   if (!(b > -INFINITY)) return 0;
   const double z = exp_wide(sigmoid ? -(double)x : (double)x - (double)m);
   const double s = sigmoid ? 1.0 / (1.0 + z) : z / total;
-  return (sortable(s + (double)b) & ~1023ull) | (uint64_t)(1023 - e);
+  return sortable(s + (double)b);
 }
 // A row's sum of exponentials in 64 bits.
 template <typename T, int LANES, int V>
@@ -362,22 +362,24 @@ __device__ __forceinline__ int select_wide(const T* row, const float* bias, int 
     keys[j * 64 + lane] = key;  // (a lane reads its own alone)
   }
   int mine = -1;
-  uint64_t last = ~0ull;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
     uint64_t best = 0;
+    int at = 0;  // (a lane's experts rise with i: the first of equal keys is the lower one)
 #pragma unroll 4
     for (int i = 0; i < V; ++i) {
       const uint64_t key = keys[i * 64 + lane];
-      best = key < last && key > best ? key : best;
+      at = key > best ? i : at;
+      best = key > best ? key : best;
     }
-#pragma unroll
-    for (int d = LANES / 2; d >= 1; d >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, d);
-      best = o > best ? o : best;
-    }
-    last = best;
-    if (sub == j && best) mine = 1023 - (int)(best & 1023);
+    const uint32_t hi = group_max<LANES>((uint32_t)(best >> 32));
+    const bool top = (uint32_t)(best >> 32) == hi;
+    const uint32_t lo = group_max<LANES>(top ? (uint32_t)best : 0u);
+    const int e = expert_of<LANES>(sub, at);
+    const uint32_t first = group_max<LANES>(top && (uint32_t)best == lo && (hi | lo) ? (uint32_t)(kRouterMaxExperts - e) : 0u);
+    const int won = kRouterMaxExperts - (int)first;
+    if (sub == j && first) mine = won;
+    if (first && e == won) keys[at * 64 + lane] = 0;
   }
   return mine;
 }
@@ -539,11 +541,19 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
             int rank = 0;
 #pragma unroll
             for (int i = 0; i < LANES; ++i) rank += lt.key[grp * LANES + i] > mykey;
-            const bool chosen = mykey && rank < a.k;
-            if (chosen) lt.choice[grp * LANES + rank] = c;
+            if (mykey && rank <= a.k) lt.choice[grp * LANES + rank] = c;
             xj = -INFINITY;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             mine = lt.choice[lane];
+            // equal scores meet in one place and leave the next one empty (the one behind the last choice counts): by the index then
+            if (BIAS && __any(mine < 0 && sub <= a.k && sub < n)) {
+#pragma unroll
+              for (int i = 0; i < LANES; ++i) rank += lt.key[grp * LANES + i] == mykey && lt.expert[grp * LANES + i] < c;
+              if (mykey && rank < a.k) lt.choice[grp * LANES + rank] = c;
+              __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+              mine = lt.choice[lane];
+            }
+            mine = sub < a.k ? mine : -1;
             int ps, pj;
             place_of<LANES>(max(mine, 0), ps, pj);
             if (mine >= 0) xj = stash[pj * 64 + ps - sub];

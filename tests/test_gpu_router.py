@@ -110,6 +110,38 @@ def test_biased_scores_that_differ_in_the_tenth_place(score):
     assert (got.cpu().numpy() == U.choose64(l.astype(np.float64), score, bias, k, None)).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("score,bias,low,high", [
+    ("sigmoid", 0.0, 30.0, 33.0), ("sigmoid", 0.0, 31.0, 36.0), ("sigmoid", 0.0, 30.0, 31.0), ("sigmoid", 0.0, 28.0, 28.125),
+    ("sigmoid", 1.0, -30.0, -29.5), ("sigmoid", -1.0, 30.0, 33.0), ("softmax", 1.0, -30.5, -30.0), ("softmax", 0.5, -31.0, -30.0)])
+@pytest.mark.parametrize("E,k", [(24, 3), (256, 8), (256, 12), (700, 16)])
+def test_biased_scores_that_differ_in_the_last_places(score, bias, low, high, dtype, E, k):
+    """Scores 2^-43 to 2^-50 apart, the larger at the higher index, at the last place of the choice."""
+    l = np.full((5, E), -60.0 if bias > 0 else -6.0, np.float32)
+    for t in range(5):
+        l[t, t + 1: t + k] = 0.0 if score == "softmax" else 36.0 - low if low < 0 else 60.0
+        l[t, t + k + 1], l[t, E - 1 - t] = low, high
+    lg, b = torch.from_numpy(l).to(dtype).cuda(), np.full(E, bias, np.float32)
+    want = U.choose64(U.np64(lg), score, b, k, None)
+    assert (want[:, -1] == E - 1 - np.arange(5)).all()
+    got = P.moe_router(lg, k, score=score, bias=torch.from_numpy(b).cuda())[0]
+    assert (got.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("E,k", [(24, 8), (129, 8), (256, 8), (256, 12), (700, 8), (1000, 16)])
+@pytest.mark.parametrize("bias", [0.0, 1.0])
+def test_biased_choice_of_saturated_scores(dtype, E, k, bias):
+    """Sigmoids within e^-15 of 1, or of 0 beside a bias of 1, from logits 1/8 apart, many of them equal.  At |x| = 33 a step of
+    1/8 moves the score by 6.2e-16; a sum with 1, a quotient and their counterparts in the 64-bit form are off by
+    2^-53 (1.1e-16) each at most, so the order is the same in both."""
+    r = np.random.default_rng([E, k])
+    l = r.integers(120, 265, (33, E)) / 8.0 * (1.0 if bias == 0.0 else -1.0)
+    lg, b = torch.from_numpy(l.astype(np.float32)).to(dtype).cuda(), np.full(E, bias, np.float32)
+    got = P.moe_router(lg, k, score="sigmoid", bias=torch.from_numpy(b).cuda())[0]
+    assert (got.cpu().numpy() == U.choose64(U.np64(lg), "sigmoid", b, k, None)).all()
+
+
 def near_ties(M, E, top, score, biased, seed):
     """Logits (fp32) and biases whose `top` best experts of a row lie within a few 2^-24 of each other (their order is
     another in every row), the others well below."""
