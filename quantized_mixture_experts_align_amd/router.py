@@ -74,9 +74,9 @@ def _new_outputs(M, E, top_k, dev):
             torch.empty((M, top_k), dtype=torch.float32, device=dev))
 
 
-def _new_stats(E, dev) -> RouterStats:
+def _new_stats(E, dev, balance=(1,)) -> RouterStats:
     return RouterStats(torch.empty(E, dtype=torch.int32, device=dev), torch.empty(E, dtype=torch.float32, device=dev),
-                       torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev))
+                       torch.empty(balance, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev))
 
 
 def moe_router(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
@@ -178,14 +178,14 @@ class _ExpertsRouter(torch.autograd.Function):
     def forward(ctx, logits, bias, live, top_k, kind, renormalise, scale, means_grad, aside):
         (M, E), dev = logits.shape, logits.device
         ids, weights = _new_outputs(M, E, top_k, dev)
-        counts, means, balance, tokens = stats = _new_stats(E, dev)
+        # (the loss of no dimension from the start: a view among several outputs could not be changed in place)
+        counts, means, balance, tokens = stats = _new_stats(E, dev, ())
         work = torch.empty(router_workspace(M, E), dtype=torch.uint8, device=dev)
         _router(logits, top_k, kind, bias, live, renormalise, scale, ids, weights, stats, work)
         ctx.save_for_backward(logits, live, ids, counts, tokens)
         ctx.how = (kind, top_k, renormalise, scale)
         ctx.set_materialize_grads(False)
         aside += (ids, counts, means)
-        balance = balance.view(())
         return (weights, balance, means) if means_grad else (weights, balance)
 
     @staticmethod

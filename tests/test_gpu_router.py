@@ -324,6 +324,24 @@ def test_differentiable_form():
     empty.balance.backward()
 
 
+def test_outputs_changed_in_place():
+    """The loss, the weights and the means are tensors of their own: a program may scale or add to them in place."""
+    lg = U.logits(20, 16, F32, 3).cuda().requires_grad_(True)
+    for means_grad in (False, True):
+        rt = P.moe_experts_router(lg, 4, means_grad=means_grad)
+        grad = lambda t: torch.autograd.grad(t, lg, retain_graph=True)[0]  # noqa: E731
+        want, value = grad(0.25 * rt.balance), float(rt.balance.detach())
+        aux = rt.balance
+        aux.mul_(0.25)
+        aux += 1.0
+        assert aux.dim() == 0 and abs(float(aux.detach()) - (0.25 * value + 1.0)) <= 4 * U32 * (value + 1.0)
+        assert torch.equal(grad(aux), want)
+        for t in (rt.weights, rt.means) if means_grad else (rt.weights,):
+            want = grad((2.0 * t).sum())
+            t.mul_(2.0)
+            assert torch.equal(grad(t.sum()), want)
+
+
 def test_replayed_graphs_and_two_streams():
     """A captured forward and gradient on changing logits, two graphs with a workspace each replayed side by side."""
     M, E, k = 200, 128, 4
