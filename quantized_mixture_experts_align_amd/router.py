@@ -17,6 +17,7 @@ from . import _lib as L
 from .experts import _BF16, _F32, _I32, _call, _check, _ld
 
 _LOGITS = (torch.bfloat16, torch.float32)
+_GRAD_TOKENS, _GRAD_NORM_COLUMNS = 1 << 24, 12288   # moe_combine_grad's limits
 
 
 class RouterStats(NamedTuple):
@@ -316,9 +317,18 @@ def moe_experts_combine(y: torch.Tensor, topk_weights: torch.Tensor, slot_local_
     """Differentiable moe_combine: out bf16 [M, H] from the slots' rows y bf16 [M * k, H] and the weights
     float32 [M, k] (the router's), optionally after the post-expert RMSNorm of weight norm_w bf16 [H] (the weight
     itself, moe_norm_weight's 1 + w).  Gradients flow to y, topk_weights and norm_w; they are once differentiable
-    and zero for dead slots (slot_local_ids < 0).
+    and zero for dead slots (slot_local_ids < 0).  With a gradient M is less than 2^24 tokens, and H at most 12288 columns
+    for norm_w's.
 
     Forward and backward can be captured into a graph; as with any autograd work, hold no graph of an eager call of
     the same leaves while capturing."""
     _check_combine(y, topk_weights, slot_local_ids, norm_w)
+    M, H = topk_weights.shape[0], y.shape[1]
+    if (M >= _GRAD_TOKENS or H > _GRAD_NORM_COLUMNS) and torch.is_grad_enabled():
+        # (what the backward pass would refuse is refused before the forward one)
+        d_norm = norm_w is not None and norm_w.requires_grad
+        if M >= _GRAD_TOKENS and (y.requires_grad or topk_weights.requires_grad or d_norm):
+            raise ValueError(f"{M} tokens: moe_combine_grad takes less than 2^24")
+        if H > _GRAD_NORM_COLUMNS and d_norm:
+            raise ValueError(f"norm_w of {H} columns: moe_combine_grad gives the gradient of at most {_GRAD_NORM_COLUMNS}")
     return _ExpertsCombine.apply(y, topk_weights, norm_w, slot_local_ids, eps, routed_scaling_factor)

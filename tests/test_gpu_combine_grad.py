@@ -113,6 +113,23 @@ def test_differentiable_form(norm):
     assert not norm or float(leaves[2].grad.abs().max()) == 0.0     # no tokens, no share
 
 
+def test_a_step_whose_gradient_would_be_refused_is_refused_at_once():
+    y, g, local, _, n = (t.cuda() for t in inputs(2, 2, 16384, 5))
+    n.requires_grad_(True)
+    with pytest.raises(ValueError, match="12288"):
+        P.moe_experts_combine(y, g, local, norm_w=n)
+    with torch.no_grad():
+        assert P.moe_experts_combine(y, g, local, norm_w=n).shape == (2, 16384)
+    y.requires_grad_(True)                                          # the others' gradients have no such limit
+    P.moe_experts_combine(y, g, local, norm_w=n.detach()).sum().backward()
+    M = 1 << 24
+    y, g = torch.zeros((M, 8), dtype=torch.bfloat16, device="cuda"), torch.zeros((M, 1), device="cuda")
+    local = torch.zeros((M, 1), dtype=torch.int32, device="cuda")
+    assert P.moe_experts_combine(y, g, local).shape == (M, 8)
+    with pytest.raises(ValueError, match="2\\^24"):
+        P.moe_experts_combine(y.requires_grad_(True), g, local)
+
+
 def test_offsets_past_four_gigabytes():
     """y of 4.3 GB: the last token's gradients are those of a batch of its own."""
     M, k, H = 65600, 8, 4096
