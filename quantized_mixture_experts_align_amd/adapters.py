@@ -37,7 +37,10 @@ def moe_adapters_add(base: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: to
 
     `align` is what moe_align returns for the rows' adapter ids [numel, 1] (expert_start 0, n_local n) with the same
     block_m.  `out`: base itself, or memory apart from it (allocated when not given); it may be x or lie over it.
-    `work`: float32 workspace of adapters_workspace(numel, n, r, K, block_m) values (allocated when not given)."""
+    `work`: float32 workspace of adapters_workspace(numel, n, r, K, block_m) values (allocated when not given).
+
+    For serving: the result has no gradient.  (Where autograd has kept an `out` from before, its backward pass refuses it
+    as changed in place.)"""
     _check(base, "base", _BF16, rows=True)
     dev, (numel, N) = base.device, base.shape
     _check(x, "x", _BF16, dev=dev, rows=True)
@@ -58,8 +61,11 @@ def moe_adapters_add(base: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: to
     live = _live_ptr(local, numel, dev)
     if out is None:
         out = torch.empty((numel, N), dtype=torch.bfloat16, device=dev)
-    elif out is not base:
-        _check(out, "out", _BF16, (numel, N), dev, rows=True)
+    else:
+        if out is not base:
+            _check(out, "out", _BF16, (numel, N), dev, rows=True)
+        if not out.is_inference():
+            torch.autograd.graph.increment_version(out)
     if work is None:
         work = torch.empty(adapters_workspace(numel, n, r, K, block_m), dtype=torch.float32, device=dev)
     else:

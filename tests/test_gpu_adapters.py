@@ -205,6 +205,24 @@ def test_replayed_graphs_with_workspaces_of_their_own():
             assert torch.equal(out, P.moe_adapters_add(base, x, A, Bm, batches[(turn + i) % 4], B, scales=s)), (turn, i)
 
 
+def test_a_base_that_autograd_holds_is_known_to_have_changed():
+    d = make(20, 3, 16, 64, 64, 24)
+    w = torch.ones((20, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    for into, mode in ((None, torch.enable_grad), (None, torch.no_grad), (torch.zeros_like(w).detach(), torch.enable_grad)):
+        y = d["base"].cuda()
+        z = w * (y if into is None else into)                       # (keeps it for w's gradient)
+        with mode():
+            call(d, 16, base=y, out=y if into is None else into)
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            z.sum().backward()
+    want = call(d, 16)
+    with torch.inference_mode():
+        y = d["base"].cuda()
+        assert torch.equal(call(d, 16, base=y, out=y), want)
+        y = d["base"].cuda()
+    assert torch.equal(call(d, 16, base=y, out=y), want)            # a tensor of inference mode, outside of it
+
+
 def test_refusals_of_the_wrapper():
     d = make(12, 2, 8, 64, 64, 21)
     al, _ = aligned(d["ids"].reshape(-1, 1), 0, 2, 16)
