@@ -510,12 +510,15 @@ static int adapter_splits(int64_t row_blocks, int r, int K) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({kAdGroups / groups, by_k, kAdMaxSplits}));
 }
 
-// Whether the rows from p on reach into the memory between the first and the last of those from q on.
+// Whether matrices of rows may share memory: their spans meet, and they are not different columns of the same rows.
 static bool rows_meet(const uint16_t* p, int64_t rows, int64_t ld, int32_t cols, const uint16_t* q, int64_t rows_q, int64_t ld_q,
                       int32_t cols_q) {
   const uintptr_t p0 = (uintptr_t)p, p1 = p0 + ((rows - 1) * ld + cols) * 2, q0 = (uintptr_t)q,
                   q1 = q0 + ((rows_q - 1) * ld_q + cols_q) * 2;
-  return p0 < q1 && q0 < p1;
+  if (p1 <= q0 || q1 <= p0) return false;
+  if (ld != ld_q) return true;
+  const uintptr_t row = (uintptr_t)ld * 2, d = (p0 <= q0 ? q0 - p0 : row - (p0 - q0) % row) % row;  // q's columns behind p's
+  return !(d >= (uintptr_t)cols * 2 && d + (uintptr_t)cols_q * 2 <= row);
 }
 
 static int adapter_sizes(const char* fn, int64_t numel, int32_t L, int32_t r, int32_t N, int32_t K, int32_t block_m) {

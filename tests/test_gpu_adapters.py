@@ -120,6 +120,21 @@ def test_out_over_x_of_several_choices():
     check(d, call(d, 16, x=x, out=out), "out around x")
 
 
+def test_out_in_other_columns_of_bases_rows():
+    """base, out and x as columns of one buffer's rows: they share no element."""
+    d = make(40, 4, 16, 200, 200, 26)
+    buf = torch.full((40, 640), 9.0, dtype=torch.bfloat16, device="cuda")
+    base, out, x = buf[:, 208:408], buf[:, :200], buf[:, 416:616]
+    base.copy_(d["base"]), x.copy_(d["x"])
+    for o in (out, buf[:, 8:208]):
+        check(d, call(d, 16, base=base, x=x, out=o), "columns")
+    assert torch.equal(base.cpu(), d["base"]) and torch.equal(x.cpu(), d["x"])
+    assert bool((buf[:, 616:] == 9.0).all()) and bool((buf[:, 408:416] == 9.0).all())
+    for o in (buf[:, 16:216], buf[:, 400:600]):
+        with pytest.raises(ValueError, match="overlaps base"):
+            call(d, 16, base=base, x=x, out=o)
+
+
 def test_no_row_all_rows_and_one_row_of_an_adapter():
     for none in (1.0, 0.0):
         d = make(33, 3, 8, 64, 64, 12, none=none)
