@@ -781,7 +781,7 @@ __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradArgs a, int 
         const float z = exp_neg(-fabsf(x[j]));
         g *= (x[j] >= 0.0f ? z : 1.0f) * __builtin_amdgcn_rcpf(1.0f + z);
       }
-      v = fmaf(q[j], g - rest, v);
+      v = x[j] > -INFINITY ? fmaf(q[j], g - rest, v) : v;  // (0 of padding and of -inf, also where g is not finite)
     }
     out[j] = bad ? NAN : v;
   }

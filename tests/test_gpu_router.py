@@ -221,6 +221,25 @@ def test_nan_and_infinite_logits(score, renorm, biased):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_gradient_zeros_beside_a_gradient_that_is_not_finite(dtype, score, renorm, value):
+    M, E, k = 30, 20, 3
+    lg = U.logits(M, E, dtype, 12)
+    lg[:, 4] = -float("inf")
+    live = (torch.arange(M) % 3 - 1).to(torch.int32)
+    how = dict(score=score, renormalise=renorm, live=live.cuda())
+    ids, w, st = P.moe_router(lg.cuda(), k, stats=True, **how)
+    dw = torch.full_like(w, value)
+    for kw in (dict(d_weights=dw), dict(d_weights=dw, d_balance=torch.full((1,), value, device="cuda")),
+               dict(d_weights=None, d_means=torch.full((E,), value, device="cuda"))):
+        g = P.moe_router_grad(lg.cuda(), ids, stats=st, **kw, **how)
+        assert not bool(g[live.cuda() < 0].ne(0.0).any()) and not bool(g[:, 4].ne(0.0).any())
+        assert not bool(g[live.cuda() >= 0].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("E", [64, 129, 256])
 def test_strided_and_unaligned_rows(dtype, E):
     r = np.random.default_rng(E)
