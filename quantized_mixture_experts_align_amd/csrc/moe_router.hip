@@ -441,7 +441,14 @@ __global__ __launch_bounds__(STATS ? kRouterStatThreads : kRouterThreads) void r
     if (a.E < LANES * V || __any(!live)) mask_logits<LANES, V>(sub, live ? a.E : 0, x);
     if constexpr (BIAS) load_logits<float, LANES, V>(a.bias, sub, a.E, wide & 4, reinterpret_cast<float*>(lkeys[wv]), lane, b);
     bool bad;
-    const float m = row_max<LANES, V>(x, a.sigmoid, grp, bad);
+    float m = row_max<LANES, V>(x, a.sigmoid, grp, bad);
+    if (BIAS && !a.sigmoid && __any(bad)) {  // (the largest beside a NaN of the same lane: biased scores depend on it)
+      m = x[0];
+#pragma unroll
+      for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
+      m = group_max<LANES>(m);
+      m = m > -INFINITY ? m : 0.0f;
+    }
     float total = 0.0f, u[V];  // every expert's share, where it is needed
     if (STATS || (!a.sigmoid && (BIAS || !a.renorm))) total = row_shares<LANES, V>(x, a.sigmoid, m, u);
     // the choice: lane j of the group keeps the j-th

@@ -240,6 +240,20 @@ def test_gradient_zeros_beside_a_gradient_that_is_not_finite(dtype, score, renor
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("E,k", [(8, 7), (64, 8), (64, 12), (256, 4)])
+def test_a_nan_does_not_hide_the_rows_largest_logit(dtype, E, k):
+    """Softmax with a bias: the row's weights are NaN, and its other experts are chosen as without it."""
+    lg = U.logits(6, E, dtype, 14)
+    lg[:, 2] = 200.0
+    clean = lg.clone()
+    clean[3, 1], lg[3, 1] = -float("inf"), float("nan")
+    bias = torch.from_numpy(0.01 * np.random.default_rng(1).standard_normal(E).astype(np.float32)).cuda()
+    ids, w = P.moe_router(lg.cuda(), k, bias=bias)
+    want, cw = P.moe_router(clean.cuda(), k, bias=bias)
+    assert torch.equal(ids, want) and bool(w[3].isnan().all()) and torch.equal(w[:3], cw[:3])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("E", [64, 129, 256])
 def test_strided_and_unaligned_rows(dtype, E):
     r = np.random.default_rng(E)
