@@ -329,9 +329,9 @@ template <bool BIAS>
 __device__ __forceinline__ uint64_t wide_key(float x, float b, int e, int sigmoid, float m, double total) {
   if (!(x > -INFINITY)) return 0;
   if (!BIAS) return ((uint64_t)sortable(x) << 32) | (uint32_t)(1023 - e);
-  if (!(b > -INFINITY)) return 0;
+  if (!(b > -INFINITY) || (!sigmoid && x == INFINITY)) return 0;  // (an infinite logit's softmax is NaN, the others' beside it 0)
   const double z = exp_wide(sigmoid ? -(double)x : (double)x - (double)m);
-  const double s = sigmoid ? 1.0 / (1.0 + z) : z / total;
+  const double s = sigmoid ? 1.0 / (1.0 + z) : total > 0.0 ? z / total : 0.0;
   return sortable(s + (double)b);
 }
 // A row's sum of exponentials in 64 bits.

@@ -254,6 +254,24 @@ def test_a_nan_does_not_hide_the_rows_largest_logit(dtype, E, k):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("E,k", [(24, 8), (24, 12), (129, 4), (700, 16)])
+def test_an_infinite_logit_under_a_softmax_with_a_bias(dtype, E, k):
+    """Its own score is NaN and never chosen, the others' are 0 (their biases decide), and the row's weights are NaN: the
+    same for every top_k and wherever two biases are close or equal."""
+    r = np.random.default_rng([E, k])
+    lg = U.logits(6, E, dtype, 15)
+    lg[1, 9], lg[4, 0], lg[4, 20] = float("inf"), float("inf"), float("inf")
+    for bias in (r.standard_normal(E), np.zeros(E), 1.0 + r.permutation(E) * 2.0 ** -23):
+        bias = bias.astype(np.float32)
+        ids, w = P.moe_router(lg.cuda(), k, bias=torch.from_numpy(bias).cuda())
+        for t in (1, 4):
+            left = [e for e in range(E) if float(lg[t, e]) < float("inf")]
+            want = sorted(left, key=lambda e: (-bias[e], e))[:k]
+            assert ids[t].tolist() == want and bool(w[t].isnan().all())
+        assert bool(w[[0, 2, 3, 5]].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("E", [64, 129, 256])
 def test_strided_and_unaligned_rows(dtype, E):
     r = np.random.default_rng(E)
