@@ -250,3 +250,89 @@ def test_refusals_of_the_wrapper():
                          (dict(align=(*al[:3], al[3][:3])), "slot_local_ids"), (dict(top_k=2), "rows")):
         with pytest.raises(ValueError, match=text):
             P.moe_adapters_add(**{**ok, **change})
+
+
+# r, K: on both sides of the sizes at which few rows take one launch instead of two, in each width of the staged columns
+@pytest.mark.parametrize("r", [16, 24, 32, 64, 72])
+@pytest.mark.parametrize("numel,K,B", [(1, 264, 16), (1, 8200, 16), (40, 264, 16), (40, 4104, 16), (40, 264, 64), (300, 1032, 32)])
+def test_ranks_of_their_own_in_both_forms(r, numel, K, B):
+    """What stands behind an adapter's own rank -- here NaN -- is not used."""
+    n = 5
+    d = make(numel, n, r, 520, K, 7 * r + numel, none=0.1 if numel > 1 else 0.0)
+    if numel > 1:
+        d["ids"][:n] = np.arange(n)
+    d["ranks"] = torch.tensor([r - 1, 1, 7, 9, 0], dtype=torch.int32)
+    for a, own in enumerate(d["ranks"].tolist()):
+        d["A"][a, own:], d["B"][a, :, own:] = float("nan"), float("nan")
+    clean = {**d, "A": d["A"].nan_to_num(0.0), "B": d["B"].nan_to_num(0.0)}
+    check(clean, call(d, B), f"ranks r={r} numel={numel} K={K} B={B}")
+
+
+FORMS = [(24, 2, 64, 16), (24, 2, 8200, 16), (70, 3, 264, 64), (70, 3, 264, 32)]   # rows, adapters, K, block_m
+
+
+@pytest.mark.parametrize("numel,n,K,B", FORMS)
+def test_infinities_stale_entries_and_strided_rows_in_both_forms(numel, n, K, B):
+    d = make(numel, n, 16, 136, K, 31)
+    d["ids"][5], d["ids"][6] = 0, 1
+    al, _ = aligned(d["ids"].reshape(-1, 1), 0, n, B)
+    end = int(al[2])
+    al[0][end:] = 3                                   # entries of an earlier, longer batch
+    al[1][end // B:] = 1
+    base, x = strided(d["base"], 168), strided(d["x"], K + 16)
+    into = torch.full((numel, 160), 5.0, dtype=torch.bfloat16, device="cuda")
+    args = (d["A"].cuda(), d["B"].cuda(), al, B, d["scales"].cuda())
+    got = P.moe_adapters_add(base, x, *args, out=into[:, :136])
+    check(d, got, "strided, stale")
+    assert bool((into[:, 136:] == 5.0).all())
+    x[5, 9], x[6, 3] = float("inf"), float("nan")     # their own rows alone
+    bad = P.moe_adapters_add(base, x, *args)
+    rows = [m for m in range(numel) if m not in (5, 6)]
+    assert torch.equal(bad[rows], got[rows])
+    assert not bool(bad[5].isfinite().any()) and bool(bad[6].isnan().all())
+
+
+@pytest.mark.parametrize("numel,n,r,K,B,two", [(1, 1, 16, 8456, 16, True), (96, 6, 16, 1032, 16, False), (96, 6, 16, 4104, 16, True),
+                                               (130, 3, 64, 520, 64, True), (90, 4, 200, 264, 32, True)])
+def test_replayed_graphs_in_both_forms(numel, n, r, K, B, two):
+    """Two graphs with a workspace each, replayed side by side; what a workspace holds before a replay is not used."""
+    N = 264
+    d = make(numel, n, r, N, K, 33)
+    base, x, A, Bm, s = (d[key].cuda() for key in ("base", "x", "A", "B", "scales"))
+    batches = [aligned(np.random.default_rng(t).integers(-1 if numel > 1 else 0, n, (numel, 1)).astype(np.int32), 0, n, B)[0]
+               for t in range(4)]
+    sets = []
+    for i in range(2):
+        al, out = tuple(t.clone() for t in batches[i]), torch.empty_like(base)
+        work = torch.empty(P.adapters_workspace(numel, n, r, K, B), device="cuda")
+        run = lambda al=al, out=out, work=work: P.moe_adapters_add(base, x, A, Bm, al, B, scales=s, out=out, work=work)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        sets.append((graph, al, out, work, torch.cuda.Stream()))
+    for turn in range(4):
+        for i, (_, al, _, work, _) in enumerate(sets):
+            for t, v in zip(al, batches[(turn + i) % 4]):
+                t.copy_(v)
+            work.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for graph, _, _, _, stream in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for i, (_, _, out, work, _) in enumerate(sets):
+            want = P.moe_adapters_add(base, x, A, Bm, batches[(turn + i) % 4], B, scales=s)
+            assert torch.equal(out, want), (turn, i)
+            assert bool(work.isnan().all()) != two    # (of two launches: the inner products went through it)
+
+
+def test_two_launches_of_rows_past_four_gigabytes():
+    numel, ld = 48, 1 << 26
+    d = make(numel, 3, 64, 128, 264, 35)
+    far = lambda t: torch.as_strided(torch.empty((numel - 1) * ld + t.shape[1], dtype=torch.bfloat16, device="cuda"),  # noqa: E731
+                                     t.shape, (ld, 1)).copy_(t.cuda())
+    out = far(torch.zeros((numel, 128)))
+    check(d, call(d, 16, base=far(d["base"]), x=far(d["x"]), out=out), "far rows")
+    torch.cuda.empty_cache()
