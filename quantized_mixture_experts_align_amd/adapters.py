@@ -19,6 +19,8 @@ import torch
 from . import _lib as L
 from .experts import _BF16, _F32, _I32, _call, _check, _check_align, _ld, _live_ptr
 
+_changed = torch._C._increment_version   # (torch.autograd.graph's function without its own checks: 0.3 us, not 0.7)
+
 
 @functools.lru_cache(maxsize=256)
 def adapters_workspace(numel: int, n_adapters: int, rank: int, K: int, block_m: int) -> int:
@@ -65,7 +67,7 @@ def moe_adapters_add(base: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: to
         if out is not base:
             _check(out, "out", _BF16, (numel, N), dev, rows=True)
         if not out.is_inference():
-            torch.autograd.graph.increment_version(out)
+            _changed((out,))
     if work is None:
         work = torch.empty(adapters_workspace(numel, n, r, K, block_m), dtype=torch.float32, device=dev)
     else:
