@@ -543,12 +543,14 @@ static void launch_adapters(const AdapterArgs& a, int64_t copies, hipStream_t st
   hipLaunchKernelGGL((adapters_outer_kernel<MT, FR>), dim3((unsigned)(a.row_blocks * strips + copies)), dim3(256), 0, st, a,
                      (int)strips);
 }
-// Where one launch is the better, and right: a workgroup that has stored its columns must not have stored over x, which the tile's
-// other workgroups may still be reading (two launches are done with x before the first store).  The workgroups of a row tile each make all of its t, at some 110 GB/s, so few tiles and short
-// rows of A.  Against two launches, replayed from a graph, rank 16, N 4096, one row: K 512 4.3 us against 6.7, 2048 5.4 and 7.2, 4096 6.6 and
-// 7.6, 7168 8.2 and 8.1, 14336 12.3 and 7.2; rank 32: 2048 6.8 and 8.1, 4096 8.6 and 8.0.  16 rows of 8 adapters: the same up to 4096, 7168
-// 9.8 and 8.4; 32 of 32: 2048 9.9 and 7.9; 64 of 64, K 512: 5.1 and 7.5; 256 of 256, K 512: 9.0 and 11.4.  (Calls that are not captured
-// save the second launch's 3 us of host time besides.)
+// Where one launch is right, and the better.  Right: a workgroup that stores its columns must not store over x, which the tile's
+// other workgroups may still be reading (two launches are done with x before the first store).  Better: the workgroups
+// of a row tile each make all of its t, at some 110 GB/s, so few tiles and short rows of A.  Against two launches, replayed from a
+// graph, N 4096, one row of rank 16: K 512 4.2 us against 6.7, 2048 5.3 and 7.1, 4096 6.5 and 7.4, 6144 7.7 and 7.8, 7168 8.2 and 8.0, 8184 8.6 and
+// 7.2, 14336 12.3 and 7.2; of rank 32: 2048 6.7 and 7.9, 4096 8.4 and 7.9, 8184 12.0 and 8.5.  16 rows of 8 adapters, rank 16: 4096 6.6 and 7.5;
+// rank 32: 2048 6.8 and 8.0, 4096 9.8 and 8.1.  64 of 64, K 512: rank 16 5.1 and 8.1, rank 32 8.4 and 10.8; 256 of 256: 11.0 and 14.5, 15.7
+// and 18.8.  A call that is not captured saves the second launch's 3 us of host time besides, and for a single tile the bound goes by
+// that: replays would change to two launches at K 6144 (rank 32: between 2048 and 4096).
 static bool few_rows(const AdapterArgs& a) {
   const int64_t values = (int64_t)(a.r <= 16 ? 16 : 32) * a.K;
   return !a.over_x && a.r <= 32 && (a.row_blocks == 1 ? values < (1 << 17) : a.row_blocks <= 16 ? values <= (1 << 16) : a.K <= 512);

@@ -21,7 +21,7 @@ constexpr int kCgMaxTopK = 16;
 constexpr int kCgParts = 512;      // workgroups that leave partial sums of dn, at most (4096 x 8 x 4096: 256 take 112 us in the
                                    // place of 96; 1024 no fewer, and dn 7.2 in the place of 4.6)
 constexpr int kCgGrid = 1 << 20;    // workgroups at most (2^32 threads are a launch's limit); they stay for more tokens
-constexpr int kCgMaxNormH = 12288; // columns whose dn a workgroup can hold in LDS
+constexpr int kCgMaxNormH = 12288; // columns of dn: 48 KB of LDS, so that three workgroups stand on a CU
 
 struct CombineGradArgs {
   const uint16_t* y;

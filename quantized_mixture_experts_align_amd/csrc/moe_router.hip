@@ -12,11 +12,12 @@
 // (no loads, no branches; taking the largest of the group k times, with a dependent exchange each, took 47 us in the place of 20).
 // bf16 logits fit such a key whole.  fp32 logits and biased scores do not: they are cut to steps of 2^-19 and 2^-23
 // (E <= 256) below the row's largest, and a wave in which two of the k + 1 largest stand closer than the keys' errors
-// orders the candidates again by keys of 64 bits.
+// orders the candidates again by keys of 64 bits, and where scores are equal in all of those by the index.
 //
-// Bound: the launch for small batches (1 token 3.6 us, 64 tokens 3.1 us), vector instructions for large ones: 32768 x 256
-// bf16 sigmoid + bias, top 8, take 18 us (854 instructions a wave of 4 tokens, 88 % of the time issuing; the 19 MB
-// alone would take 3.7), 11 without the bias.  The gradient of 32765 x 129 fp32 takes 16 us (its 30 MB 6).
+// Bound: the launch for small batches (1 token 3.5 us, 64 tokens 3.0 us), vector instructions for large ones: 32768 x 256
+// bf16 sigmoid + bias, top 8, take 17 us (842 instructions a wave of 4 tokens, 88 % of the time issuing; the 19 MB
+// alone would take 3.7), 11 without the bias, 24 with biases of 0 (in most waves two scores are equal).  The gradient of
+// 32765 x 129 fp32 takes 14 to 16 us (its 30 MB 6).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

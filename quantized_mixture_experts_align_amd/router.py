@@ -318,7 +318,8 @@ def moe_experts_combine(y: torch.Tensor, topk_weights: torch.Tensor, slot_local_
     float32 [M, k] (the router's), optionally after the post-expert RMSNorm of weight norm_w bf16 [H] (the weight
     itself, moe_norm_weight's 1 + w).  Gradients flow to y, topk_weights and norm_w; they are once differentiable
     and zero for dead slots (slot_local_ids < 0).  With a gradient M is less than 2^24 tokens, and H at most 12288 columns
-    for norm_w's.
+    for norm_w's.  All four tensors are read again in the backward pass: write over copies of them (what kernels write,
+    a reused align's outputs among it, autograd does not see).
 
     Forward and backward can be captured into a graph; as with any autograd work, hold no graph of an eager call of
     the same leaves while capturing."""
