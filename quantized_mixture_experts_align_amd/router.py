@@ -213,9 +213,9 @@ def moe_experts_router(logits: torch.Tensor, top_k: int, score: str = "softmax",
     E * sum_e (counts_e / sum counts) * means_e; for counts that are summed over several ranks' batches form the same
     sum from `means` (the ranks' mean of it is the loss of the whole batch when they hold equally many tokens).
 
-    ids and counts are read again in the backward pass (counts for the gradient of balance alone): write over copies of
-    them.  Forward and backward can be captured into a graph; as with any autograd work, hold no graph of an eager call
-    of the same leaves while capturing."""
+    logits, live, ids and counts (for the gradient of balance and means alone) are read again in the backward pass: write
+    over copies of them.  Forward and backward can be captured into a graph; as with any autograd work, hold no graph of
+    an eager call of the same leaves while capturing."""
     kind = _score(score)
     _check_logits(logits, top_k, bias, live)
     if not 1 <= top_k <= logits.shape[1]:
